@@ -1,0 +1,208 @@
+// attend.cuh -- what the attention kernels over the 8-bit cache share: the
+// tiles of query rows, their division among the CTAs, and the table that
+// translates a tile's keys to cache tokens.
+//
+// Mathematics.  With codes K, V, a token's scales ks, vs, and a row's query q:
+//   t_j = scale * log2(e) * ks_j * (q . K_j)         (base-2 logarithms)
+//   o   = sum_j 2^{t_j} vs_j V_j / sum_j 2^{t_j}.
+// The value scale is a power of two (or any positive number) per token, so it
+// goes into the exponent: with u_j = t_j + log2 vs_j and a running reference
+// m >= max u_j - slack,
+//   acc = sum_j 2^{u_j - m + kHead} V_j,   l = sum_j 2^{u_j - m + kHead} / vs_j,
+//   o = acc / l,   log sum_j e^{...} = ln2 * (m - kHead + log2 l).
+// The weights 2^{u_j - m + kHead} lie below 2^{kHead + slack} <= 2^15 and are
+// rounded to FP16 for the matrix instruction: 11 bits, and a weight vanishes
+// only below 2^{-25-kHead} of the largest.  V_j are the bare codes, exact in FP16.
+#pragma once
+
+#include "cache.h"
+
+namespace hwr {
+
+constexpr float kHead = 7.f;    // weights are 2^kHead at the reference
+constexpr float kSlack = 8.f;   // a row's reference rises once it is exceeded by this much
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttendParams {
+  CacheView c;
+  SeqView s;
+  const uint8_t* q;
+  int64_t q_stride;        // bytes
+  uint8_t* out;
+  float* lse;
+  const int32_t* sel_idx;
+  const int32_t* sel_len;
+  int32_t sel_width;
+  int32_t causal;
+  int32_t Hq, G;           // query heads, and query heads per key/value head
+  float scale_log2;        // scale * log2(e)
+  int32_t max_keys;        // positions that the page table can hold
+  int32_t n_tiles;         // tile slots
+  int32_t sel_tiles;       // tiles of one query (selection)
+  int32_t n_ctas;          // CTAs that share the units, or 0: one CTA per (tile, head)
+  int32_t* prefix;         // [n_tiles + 1] unit counts before each tile (workspace)
+  float* part_o;           // [2 n_ctas][rows][D]
+  float2* part_ml;         // [2 n_ctas][rows]: reference and sum
+  uint32_t* status;
+};
+
+// A tile: up to R consecutive rows of one sequence's (query, head in group)
+// pairs, query-major; with a selection, rows of one query.
+struct Tile {
+  int b;         // sequence
+  int q0;        // first activation row of the sequence
+  int first;     // first (query, head) pair, counted from the sequence's first
+  int rows;      // pairs
+  int n_q;       // queries of the sequence
+  int len;       // its length
+  int n_keys;    // entries to go over: positions, or entries of the selection
+  int row;       // the query's activation row (selection)
+};
+
+template <int R>
+__device__ __forceinline__ Tile tile_at(const AttendParams& p, int t) {
+  Tile x;
+  x.rows = 0;
+  x.n_keys = 0;
+  x.row = 0;
+  if (p.sel_width) {
+    const int r = t / p.sel_tiles, part = t - r * p.sel_tiles;
+    if (r >= seq_row(p.s, p.s.B)) return x;
+    x.b = slot_owner(p.s, r, 1, 1, 0);
+    x.q0 = seq_row(p.s, x.b);
+    x.n_q = seq_row(p.s, x.b + 1) - x.q0;
+    x.len = __ldg(p.s.kv_len + x.b);
+    x.row = r;
+    x.first = (r - x.q0) * p.G + part * R;
+    x.rows = min(R, p.G - part * R);
+    if (r < x.q0) x.rows = 0;
+    x.n_keys = min(max(__ldg(p.sel_len + r), 0), p.sel_width);
+    return x;
+  }
+  x.b = slot_owner(p.s, t, p.G, R, 1);
+  x.q0 = seq_row(p.s, x.b);
+  x.n_q = seq_row(p.s, x.b + 1) - x.q0;
+  x.len = __ldg(p.s.kv_len + x.b);
+  const int64_t i = t - slot_base(p.s, x.b, p.G, R, 1);
+  const int64_t left = static_cast<int64_t>(x.n_q) * p.G - i * R;
+  if (i < 0 || left <= 0) return x;
+  x.first = static_cast<int>(i * R);
+  x.rows = static_cast<int>(min(left, static_cast<int64_t>(R)));
+  int n = x.len;
+  if (p.causal) n = x.len - x.n_q + (x.first + x.rows - 1) / p.G + 1;
+  x.n_keys = min(max(n, 0), p.max_keys);
+  if (n > p.max_keys && p.status) atomicOr(p.status, kStatusToken);
+  return x;
+}
+
+// Units of UNIT keys of a tile: at least one where it has rows, so that a row
+// that sees nothing is written too.
+template <int UNIT>
+__device__ __forceinline__ int tile_units(const Tile& x) {
+  return x.rows <= 0 ? 0 : max(1, (x.n_keys + UNIT - 1) / UNIT);
+}
+
+// Number of positions that (query, head) pair `pair` of the tile's sequence sees.
+__device__ __forceinline__ int row_limit(const AttendParams& p, const Tile& x, int pair) {
+  return p.causal ? x.len - x.n_q + pair / p.G + 1 : x.len;
+}
+
+// CTA c of n <= u takes units [start(c), start(c+1)) of u: one or more each.
+__host__ __device__ __forceinline__ int64_t share_start(int64_t c, int64_t u, int64_t n) { return c * u / n; }
+__device__ __forceinline__ int64_t share_owner(int64_t unit, int64_t u, int64_t n) {
+  return ((unit + 1) * n - 1) / u;
+}
+
+// The token that key entry `e` of a tile stands for, as the kernels read it.
+struct TokenEntry {
+  uint32_t off16;  // offset of the token in the cache, in units of 16 bytes, without the head
+  int32_t pos;     // its position; INT_MAX where nothing is to be seen
+  float ks;        // key scale
+  float lvs;       // log2 of the value scale
+};
+constexpr uint32_t kNoToken = 0xFFFFFFFFu;
+
+__device__ __forceinline__ TokenEntry translate(const AttendParams& p, const Tile& x, int h, int e) {
+  TokenEntry t;
+  t.off16 = kNoToken;
+  t.pos = INT32_MAX;
+  t.ks = 0.f;
+  t.lvs = 0.f;
+  if (e >= x.n_keys) return t;
+  int pos = e;
+  if (p.sel_width) {
+    pos = __ldg(p.sel_idx + static_cast<int64_t>(x.row) * p.sel_width + e);
+    if (pos < 0 || pos >= min(x.len, row_limit(p, x, x.first))) return t;
+  }
+  int off;
+  const int64_t page = page_of(p.s, p.c, x.b, pos, &off);
+  if (page < 0) {
+    if (p.status) atomicOr(p.status, kStatusToken);
+    return t;
+  }
+  const int64_t si = (page * p.c.page_blocks + (off >> p.c.block_shift)) * p.c.heads + h;
+  t.off16 = static_cast<uint32_t>(page * p.c.page16 + off * p.c.token16);
+  t.pos = pos;
+  t.ks = __ldg(p.c.ks + si);
+  t.lvs = __log2f(fmaxf(__ldg(p.c.vs + si), kMinBlockScale));
+  return t;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;  // 0: the 16 bytes become zero, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// FP16 operands hold a query row scaled by a power of two to a largest
+// magnitude in [1, 2): exact for BF16 values down to 2^-14 of the largest, and
+// within 2^-25 of it below.  The exponent of the row's scale:
+__device__ __forceinline__ float row_pow2(float amax) {
+  int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+  if (!(amax < INFINITY)) e = 0;
+  e = min(max(e, -100), 120);
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+template <int N>
+__device__ __forceinline__ int block_scan_tiles(int v, int* total, int* warp_sums) {
+  // exclusive prefix over N threads
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFullMask, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < N / 32; ++w) {
+    const int s = warp_sums[w];
+    before += w < warp ? s : 0;
+    all += s;
+  }
+  *total = all;
+  return before + inc - v;
+}
+
+cudaError_t launch_attend_stream(const AttendParams& p, int D, bool f16, int grid, cudaStream_t stream);
+cudaError_t launch_attend_join(const AttendParams& p, int D, int R, bool f16, cudaStream_t stream);
+int attend_stream_ctas_per_sm(int D);
+
+constexpr int kStreamRows = 16;    // rows of a tile of the streaming kernel
+constexpr int kMaxSplitTiles = 512;  // tiles of a launch whose CTAs share units
+
+}  // namespace hwr

@@ -1,0 +1,376 @@
+// cache_write.cu -- what writes 8-bit rows before the indexer and the
+// attention read them: rotated FP8 rows with a scale each, and the append of
+// rotated keys and of values to a paged cache with a scale per block of tokens
+// and head.
+//
+// Both only move bytes.  A lane holds 8 consecutive dimensions (a 16-byte
+// load), so a row of D takes D/8 lanes and a warp step 256/D rows.  The
+// rotation's partner dimensions of the half-split layout lie a whole number of
+// lanes away (rot_dim is a multiple of 16) and come by shuffle; those of the
+// interleaved layout are the lane's own.
+#include "cache.h"
+
+namespace hwr {
+namespace {
+
+template <int D>
+constexpr int kLanes = D / 8;      // lanes of a row
+template <int D>
+constexpr int kRows = 256 / D;     // rows of a warp step
+
+// Cosines and sines that a lane needs for its 8 dimensions at one position.
+struct Angles {
+  float c[8], s[8];
+};
+
+// sub: the lane's index within its row.  Interleaved: entry i serves the pair (2i, 2i+1).
+__device__ __forceinline__ void load_angles(const RotView& r, int64_t pos, int sub, Angles& a) {
+  const int half = r.rot >> 1;
+  if (8 * sub >= r.rot) return;
+  const float* row = r.table + pos * r.rot;
+  if (r.inter) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * sub));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + 4 * sub));
+    a.c[0] = c.x, a.c[1] = c.y, a.c[2] = c.z, a.c[3] = c.w;
+    a.s[0] = s.x, a.s[1] = s.y, a.s[2] = s.z, a.s[3] = s.w;
+  } else {
+    const int d = 8 * sub < half ? 8 * sub : 8 * sub - half;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(row + d + 4 * i));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + d + 4 * i));
+      a.c[4 * i] = c.x, a.c[4 * i + 1] = c.y, a.c[4 * i + 2] = c.z, a.c[4 * i + 3] = c.w;
+      a.s[4 * i] = s.x, a.s[4 * i + 1] = s.y, a.s[4 * i + 2] = s.z, a.s[4 * i + 3] = s.w;
+    }
+  }
+}
+
+// The 8 values of `raw` in FP32, rotated.  Every product and sum is rounded on
+// its own (no contraction), so the result is that of the formula in FP32.
+// All 32 lanes take part.
+template <int D, bool F16>
+__device__ __forceinline__ void rotate(const RotView& r, const uint4& raw, int sub, const Angles& a, float (&y)[8]) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack_act<F16>(w[i]);
+    y[2 * i] = f.x, y[2 * i + 1] = f.y;
+  }
+  if (r.rot == 0) return;
+  if (r.inter) {
+    if (8 * sub < r.rot) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p = y[2 * i], q = y[2 * i + 1];
+        y[2 * i] = __fsub_rn(__fmul_rn(p, a.c[i]), __fmul_rn(q, a.s[i]));
+        y[2 * i + 1] = __fadd_rn(__fmul_rn(q, a.c[i]), __fmul_rn(p, a.s[i]));
+      }
+    }
+    return;
+  }
+  const int hl = r.rot >> 4;  // lanes between the two halves
+  const int lane = threadIdx.x & 31;
+  const bool first = sub < hl;
+  const bool in = sub < 2 * hl;
+  const int from = in ? (first ? lane + hl : lane - hl) : lane;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t o = __shfl_sync(kFullMask, w[i], from);
+    const float2 f = unpack_act<F16>(o);
+    const float pv[2] = {f.x, f.y};
+    if (in) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int e = 2 * i + j;
+        const float xc = __fmul_rn(y[e], a.c[e]), os = __fmul_rn(pv[j], a.s[e]);
+        // first half: a cos - b sin; second: b cos + a sin
+        y[e] = first ? __fsub_rn(xc, os) : __fadd_rn(xc, os);
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int o = kLanes<D> / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
+  return v;
+}
+
+__device__ __forceinline__ uint2 pack_codes(const float (&y)[8]) {
+  uint2 r;
+  r.x = f32x2_to_e4m3x2(y[0], y[1]) | (f32x2_to_e4m3x2(y[2], y[3]) << 16);
+  r.y = f32x2_to_e4m3x2(y[4], y[5]) | (f32x2_to_e4m3x2(y[6], y[7]) << 16);
+  return r;
+}
+
+// ------------------------------------------------------- rotated FP8 rows --
+// A warp takes 256/D tokens and a share of the heads, so a lane's cosines and
+// sines are loaded once for all of them.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __restrict__ x, int64_t S, int H,
+                                                              int64_t x_stride, const int32_t* __restrict__ positions,
+                                                              RotView rot, int heads_per, uint8_t* __restrict__ codes,
+                                                              float* __restrict__ scale, uint32_t* status) {
+  const int lane = threadIdx.x & 31, sub = lane % kLanes<D>;
+  const int64_t t = (blockIdx.x * int64_t(8) + (threadIdx.x >> 5)) * kRows<D> + lane / kLanes<D>;
+  const bool live = t < S;
+  const int h0 = blockIdx.y * heads_per, h1 = min(H, h0 + heads_per);
+  Angles a;
+  bool ok = live;
+  if (rot.rot && live) {
+    const int64_t pos = positions ? __ldg(positions + t) : t;
+    ok = pos >= 0 && pos < rot.rows;
+    if (ok) load_angles(rot, pos, sub, a);
+    if (!ok && sub == 0 && h0 == 0 && status) atomicOr(status, kStatusToken);
+  }
+  const uint8_t* row = x + t * x_stride + sub * 16;
+  constexpr int U = 4;
+  for (int h = h0; h < h1; h += U) {
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      raw[u] = ok && h + u < h1 ? __ldcs(reinterpret_cast<const uint4*>(row + (h + u) * (2 * D)))
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float y[8];
+      rotate<D, F16>(rot, raw[u], sub, a, y);
+      float m = 0.f;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m = fmaxf(m, fabsf(y[i]));
+        nan = nan || isnan(y[i]);
+      }
+      m = row_max<D>(nan ? INFINITY : m);
+      const float sc = !ok ? 1.f : m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = ok && m < INFINITY ? __fdiv_rn(y[i], sc) : NAN;
+      const uint2 code = pack_codes(y);
+      if (live && h + u < h1) {
+        const int64_t o = t * H + h + u;
+        *reinterpret_cast<uint2*>(codes + o * D + sub * 8) = code;
+        if (sub == 0) scale[o] = sc;
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------- cache append --
+// log2 of the least power of two s with amax <= 448 s = 1.75 * 2^8 s, at least
+// -100: the exponent of amax less 8, or less 7 where its fraction is above 1.75.
+__device__ __forceinline__ float block_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  if (e < -100) e = -100;  // zero and tiny blocks
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Keys and values.  CTAs [0, kv_slots * kv_split): slot = one block of tokens
+// (floor(rows/block) + 2 slots a sequence), split over the 2*heads key and
+// value heads.  A (block, head) is taken by block/16 warps (one for blocks of
+// up to 16), 16 rows each, held in registers between the maximum and the
+// quantisation: every row is read once.  Then q: 8 warps x 256/D rows x a share
+// of the query heads per CTA.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant__ AppendParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes<D>, rsub = lane / kLanes<D>;
+  const int kv_ctas = p.kv_slots * p.kv_split;
+  if (static_cast<int>(blockIdx.x) >= kv_ctas) {
+    const int i = blockIdx.x - kv_ctas;
+    const int r = (i % p.q_slots * 8 + warp) * kRows<D> + rsub;
+    const int h0 = i / p.q_slots * p.q_heads, h1 = min(p.Hq, h0 + p.q_heads);
+    Angles a;
+    bool ok = r < p.s.S && r < seq_row(p.s, p.s.B);
+    if (ok) {
+      const int b = slot_owner(p.s, r, 1, 1, 0);
+      const int pos = __ldg(p.s.kv_len + b) - (seq_row(p.s, b + 1) - r);
+      ok = pos >= 0 && (p.r.rot == 0 || pos < p.r.rows);
+      if (ok && p.r.rot) load_angles(p.r, pos, sub, a);
+      if (!ok && sub == 0 && h0 == 0 && p.status) atomicOr(p.status, kStatusToken);
+    }
+    const uint8_t* in = p.q + r * p.q_stride + sub * 16;
+    uint8_t* out = p.q_out + (static_cast<int64_t>(r) * p.Hq) * (2 * D) + sub * 16;
+    constexpr int U = 4;
+    for (int h = h0; h < h1; h += U) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        raw[u] = ok && h + u < h1 ? __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * (2 * D)))
+                                  : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float y[8];
+        rotate<D, F16>(p.r, raw[u], sub, a, y);
+        const uint4 o = make_uint4(pack_act<F16>(y[0], y[1]), pack_act<F16>(y[2], y[3]), pack_act<F16>(y[4], y[5]),
+                                   pack_act<F16>(y[6], y[7]));
+        if (ok && h + u < h1) *reinterpret_cast<uint4*>(out + (h + u) * (2 * D)) = o;
+      }
+    }
+    return;
+  }
+
+  const int slot = blockIdx.x % p.kv_slots, part = blockIdx.x / p.kv_slots;
+  const int blk = p.c.block;
+  const int b = slot_owner(p.s, slot, 1, blk, 2);
+  const int row0 = seq_row(p.s, b), row1 = seq_row(p.s, b + 1);
+  const int n_new = row1 - row0;
+  if (n_new <= 0) return;
+  const int len = __ldg(p.s.kv_len + b);
+  const int past = len - n_new;  // position of the first new token
+  // block number j of the sequence's touched blocks; its tokens [t0, t0 + blk)
+  const int j = static_cast<int>(slot - slot_base(p.s, b, 1, blk, 2));
+  const int64_t t0 = (static_cast<int64_t>(past >> p.c.block_shift) + j) * blk;  // floor for negative positions too
+  if (t0 >= len) return;
+  const int lo = static_cast<int>(max(t0, static_cast<int64_t>(past)) - t0);            // first new token in the block
+  const int hi = static_cast<int>(min(t0 + blk, static_cast<int64_t>(len)) - t0);       // end of the new tokens
+  int off = 0;
+  const int64_t page = t0 >= 0 ? page_of(p.s, p.c, b, static_cast<int>(t0), &off) : -1;
+  const bool bad_tail = p.r.rot && t0 + hi > p.r.rows;
+  if ((page < 0 || bad_tail) && threadIdx.x == 0 && part == 0 && p.status) atomicOr(p.status, kStatusToken);
+  if (page < 0) return;
+  const int hi_ok = bad_tail ? static_cast<int>(max(p.r.rows - t0, int64_t(lo))) : hi;
+  if (hi_ok <= lo) return;
+
+  const int team = blk <= 16 ? 1 : blk >> 4;   // warps of a (block, head)
+  const int teams = 8 / team, in_team = warp % team;
+  const int jobs = 2 * p.c.heads, jobs_per = (jobs + p.kv_split - 1) / p.kv_split;
+  const int j0 = part * jobs_per, j1 = min(jobs, j0 + jobs_per);
+  constexpr int STEPS = 16 / kRows<D>;  // warp steps of 16 rows
+  __shared__ float part_max[8];
+  const int64_t sc0 = (page * p.c.page_blocks + (off >> p.c.block_shift)) * p.c.heads;
+  const int64_t tok0 = page * p.c.page16 + off * p.c.token16;
+  for (int jb = j0; jb < j1; jb += teams) {
+    const int job = jb + warp / team;
+    const bool on = job < j1;
+    const bool is_v = on && job >= p.c.heads;
+    const int h = on ? (is_v ? job - p.c.heads : job) : 0;
+    const uint8_t* src = (is_v ? p.v : p.k) + h * (2 * D) + sub * 16;
+    uint4 raw[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int t = in_team * 16 + i * kRows<D> + rsub;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (on && t >= lo && t < hi_ok)
+        raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + (row0 + (t0 - past) + t) * p.kv_stride));
+    }
+    float y[STEPS][8];
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int t = in_team * 16 + i * kRows<D> + rsub;
+      const bool in = on && t >= lo && t < hi_ok;
+      RotView r = p.r;
+      if (is_v) r.rot = 0;
+      Angles a;
+      if (in && r.rot) load_angles(r, t0 + t, sub, a);
+      rotate<D, F16>(r, raw[i], sub, a, y[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = fabsf(y[i][e]);
+        const bool fin = v < INFINITY;
+        if (in && fin) m = fmaxf(m, v);
+        if (!fin) y[i][e] = NAN;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+    if (team > 1) {
+      if (lane == 0) part_max[warp] = m;
+      __syncthreads();
+      for (int w = 0; w < team; ++w) m = fmaxf(m, part_max[warp - in_team + w]);
+    }
+    float* sp = (is_v ? p.c.vs : p.c.ks) + sc0 + h;
+    const float need = block_scale(m);
+    const float old = on && lo > 0 ? *sp : 0.f;
+    const float sc = lo > 0 ? fmaxf(need, fmaxf(old, kMinBlockScale)) : need;
+    // the old scale and the maxima are read before they are overwritten
+    if (team > 1)
+      __syncthreads();
+    else
+      __syncwarp();
+    uint8_t* dst = (is_v ? p.c.v : p.c.k) + (tok0 + h * p.c.head16) * 16 + sub * 8;
+    const float inv = 1.f / sc;  // a power of two: exact
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int t = in_team * 16 + i * kRows<D> + rsub;
+      if (!on || t >= blk) continue;
+      uint2* at = reinterpret_cast<uint2*>(dst + t * p.c.token16 * 16);
+      if (t >= lo && t < hi_ok) {
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = y[i][e] * inv;
+        *at = pack_codes(z);
+      } else if (t < lo && sc != old) {
+        // an earlier token of a block whose scale rises
+        const float f = old * inv;
+        const uint2 was = *at;
+        const uint32_t ww[2] = {was.x, was.y};
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t hh = e4m3x2_to_f16x2(static_cast<uint16_t>(ww[e >> 1] >> (16 * (e & 1))));
+          const float2 v = unpack_act<true>(hh);
+          z[2 * e] = v.x * f, z[2 * e + 1] = v.y * f;
+        }
+        *at = pack_codes(z);
+      }
+    }
+    if (on && lane == 0 && in_team == 0) *sp = sc;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rotate_quantise(const void* x, int64_t S, int H, int D, bool f16, int64_t x_stride,
+                                   const int32_t* positions, const RotView& rot, uint8_t* codes, float* scale,
+                                   uint32_t* status, int sms, cudaStream_t stream) {
+  if (S == 0 || H == 0) return cudaSuccess;
+  const int64_t bx = (S + 8 * (256 / D) - 1) / (8 * (256 / D));
+  // few tokens: the heads are split over CTAs until the SMs have two each
+  int split = 1;
+  while (bx * split < 2 * sms && split * 4 <= H) split *= 2;
+  const int per = (H + split - 1) / split;
+  const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>((H + per - 1) / per));
+  const uint8_t* xb = static_cast<const uint8_t*>(x);
+#define HWR_GO(DD, FF)                                                                                            \
+  rotate_quantise_kernel<DD, FF><<<grid, 256, 0, stream>>>(xb, S, H, x_stride * 2, positions, rot, per, codes,    \
+                                                           scale, status)
+  if (D == 128) {
+    if (f16) HWR_GO(128, true); else HWR_GO(128, false);
+  } else {
+    if (f16) HWR_GO(64, true); else HWR_GO(64, false);
+  }
+#undef HWR_GO
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(AppendParams p, int D, bool f16, int sms, cudaStream_t stream) {
+  if (p.s.S == 0 || p.s.B == 0) return cudaSuccess;
+  p.kv_slots = static_cast<int32_t>(p.s.S / p.c.block + 2 * static_cast<int64_t>(p.s.B));
+  const int team = p.c.block <= 16 ? 1 : p.c.block / 16, teams = 8 / team;
+  p.kv_split = 1;
+  while (static_cast<int64_t>(p.kv_slots) * p.kv_split < 2 * sms && p.kv_split * teams < 2 * p.c.heads) p.kv_split *= 2;
+  p.q_slots = p.q_heads = 0;
+  int64_t q_ctas = 0;
+  if (p.q) {
+    p.q_slots = static_cast<int32_t>((p.s.S + 8 * (256 / D) - 1) / (8 * (256 / D)));
+    int split = 1;
+    while (static_cast<int64_t>(p.q_slots) * split < 2 * sms && split * 4 <= p.Hq) split *= 2;
+    p.q_heads = (p.Hq + split - 1) / split;
+    q_ctas = static_cast<int64_t>(p.q_slots) * ((p.Hq + p.q_heads - 1) / p.q_heads);
+  }
+  const int64_t grid = static_cast<int64_t>(p.kv_slots) * p.kv_split + q_ctas;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+#define HWR_GO(DD, FF) cache_append_kernel<DD, FF><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p)
+  if (D == 128) {
+    if (f16) HWR_GO(128, true); else HWR_GO(128, false);
+  } else {
+    if (f16) HWR_GO(64, true); else HWR_GO(64, false);
+  }
+#undef HWR_GO
+  return cudaGetLastError();
+}
+
+}  // namespace hwr

@@ -178,6 +178,13 @@ bool encode_2d(CUtensorMap* tm, const void* base, bool fp8, int64_t rows, int D,
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
+
+int current_device_sms() {
+  DeviceInfo di;
+  if (device_info(&di) != INDEXER_OK) return 0;
+  return di.sm100 ? di.sms : -1;
+}
+
 }  // namespace hwr
 
 using namespace hwr;

@@ -104,6 +104,10 @@ inline int candidate_capacity(int ksel, bool prune) {
   return c < ksel + 256 ? r128(ksel + 256) : c;
 }
 
+// SM count of the current device: 0 when a CUDA call fails, negative when the
+// device is not sm_100.
+int current_device_sms();
+
 cudaError_t launch_pool_keys(const void* k, int64_t n_pools, int D, const void* coef, int ratio, void* out,
                              cudaStream_t stream);
 cudaError_t launch_prune_setup(const void* q, const float* w, const float* q_scale, bool fp8, int64_t S, int H,

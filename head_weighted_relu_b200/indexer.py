@@ -6,13 +6,18 @@ step of the indexer runs in the library's kernels; there is no fallback.  If the
 library is missing, importing this module raises.
 
 `topk(...)` is the convenience call most users want: it allocates outputs and
-workspace with torch (plumbing) and calls indexer_topk.
+workspace with torch (plumbing) and calls indexer_topk.  Around it,
+`rotate_quantise(...)` makes its FP8 rows, `cache_append(...)` keeps the keys and
+values of new tokens in a paged 8-bit cache, and `cache_attend(...)` attends over
+that cache, over what `topk` selected or over whole sequences.
 """
 
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -36,6 +41,8 @@ EXPORTS = ("indexer_out_width", "indexer_workspace_bytes", "indexer_partition_ro
            "indexer_padded_workspace_bytes", "indexer_topk_padded",
            "indexer_witness_workspace_bytes", "indexer_topk_witness",
            "indexer_pool_keys",
+           "indexer_rotate_quantise", "indexer_cache_append",
+           "indexer_cache_attend_workspace_bytes", "indexer_cache_attend",
            "indexer_pair_overlap", "indexer_pair_regions", "indexer_read_status", "indexer_read_prune_counters",
            "indexer_status_string",
            "indexer_abi_version", "indexer_build_info")
@@ -54,6 +61,37 @@ class Problem(ctypes.Structure):
                 ("D", ctypes.c_int32), ("q_pos0", ctypes.c_int64), ("visibility", ctypes.c_int32),
                 ("ratio", ctypes.c_int32), ("K", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+ACT_BF16, ACT_FP16 = 0, 1
+STATUS_TOKEN = 8   # status bit of the cache calls: a token's page or position does not exist
+
+
+class Rotation(ctypes.Structure):
+    """Mirror of indexer_rotation."""
+    _fields_ = [("table", ctypes.c_void_p), ("rows", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class CacheDesc(ctypes.Structure):
+    """Mirror of indexer_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("block", ctypes.c_int32), ("heads", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
+class Sequences(ctypes.Structure):
+    """Mirror of indexer_sequences."""
+    _fields_ = [("S", ctypes.c_int64), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_pages", ctypes.c_int32), ("B", ctypes.c_int32)]
+
+
+class Attention(ctypes.Structure):
+    """Mirror of indexer_attention."""
+    _fields_ = [("Hq", ctypes.c_int32), ("act", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("sel_width", ctypes.c_int32), ("max_q", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 def _load():
@@ -91,6 +129,11 @@ def _load():
     lib.indexer_witness_workspace_bytes.argtypes = [P, i64, ctypes.POINTER(ctypes.c_size_t)]
     lib.indexer_topk_witness.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.indexer_pool_keys.argtypes = [vp, i64, i32, vp, i32, vp, vp]
+    lib.indexer_rotate_quantise.argtypes = [vp, i64, i32, i32, i32, i64, vp, ctypes.POINTER(Rotation), vp, vp, vp, vp]
+    CD, SQ, AT = ctypes.POINTER(CacheDesc), ctypes.POINTER(Sequences), ctypes.POINTER(Attention)
+    lib.indexer_cache_append.argtypes = [CD, SQ, vp, vp, i64, i32, ctypes.POINTER(Rotation), vp, i32, i64, vp, vp, vp]
+    lib.indexer_cache_attend_workspace_bytes.argtypes = [CD, SQ, AT, ctypes.POINTER(ctypes.c_size_t)]
+    lib.indexer_cache_attend.argtypes = [CD, SQ, AT, vp, i64, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.indexer_pair_overlap.argtypes = [vp, vp, i64, i32, vp, vp]
     lib.indexer_pair_regions.argtypes = [vp, vp, i64, i32, vp, vp, vp, vp, vp]
     lib.indexer_read_status.argtypes = [vp, ctypes.POINTER(i32), vp]
@@ -376,3 +419,249 @@ def pool_keys(k, pool_coef, ratio, stream=None):
     out = torch.empty((T // ratio, D), dtype=torch.bfloat16, device=k.device)
     indexer_pool_keys(k.contiguous(), T, D, pool_coef.contiguous(), ratio, out, stream)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Around the indexer: FP8 rows, the paged 8-bit cache, attention over it.
+# ---------------------------------------------------------------------------
+
+_ACT = {torch.bfloat16: ACT_BF16, torch.float16: ACT_FP16}
+
+
+def _act(x, what):
+    a = _ACT.get(x.dtype)
+    if a is None:
+        raise ValueError(f"{what} must be bfloat16 or float16, not {x.dtype}")
+    return a
+
+
+def _need(ok, message):
+    if not ok:
+        raise ValueError(message)
+
+
+def _tokens(x, what, device, shape=None, dtype=None):
+    """Token stride of activations [S, H, D] whose heads are packed (so a slice of
+    a wider projection passes unchanged)."""
+    _need(x.dim() == 3 and x.device == device and (dtype is None or x.dtype == dtype)
+          and (shape is None or tuple(x.shape) == tuple(shape)),
+          f"{what}: expected {'[S, H, D]' if shape is None else tuple(shape)}"
+          f"{'' if dtype is None else f' {dtype}'} on {device}, got {tuple(x.shape)} {x.dtype} on {x.device}")
+    S, H, D = x.shape
+    _need(x.numel() == 0 or ((D == 1 or x.stride(2) == 1) and (H == 1 or x.stride(1) == D)),
+          f"{what}: heads must be packed within a token (strides {x.stride()})")
+    return x.stride(0) if S > 1 else H * D
+
+
+def _ints(x, what, device, shape):
+    _need(x.dtype == torch.int32 and x.device == device and tuple(x.shape) == tuple(shape) and x.is_contiguous(),
+          f"{what} must be a contiguous {tuple(shape)} int32 tensor on {device}")
+    return x.data_ptr()
+
+
+def _rotation(table, interleaved, device):
+    if table is None:
+        return Rotation(None, 0, 0, 0)
+    _need(table.dim() == 2 and table.dtype == torch.float32 and table.is_contiguous() and table.device == device,
+          f"the rotation table must be a contiguous [positions, rot_dim] float32 tensor on {device}")
+    return Rotation(table.data_ptr(), table.shape[0], table.shape[1], 1 if interleaved else 0)
+
+
+class _On:
+    """Makes `device` current for the library call and names the stream: the
+    caller's, or the device's current one."""
+
+    def __init__(self, device, stream):
+        _need(device.type == "cuda", f"tensors must be on a CUDA device, not {device}")
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        self.guard = None
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """Rotation table [positions, rot_dim] float32 (cosines, then sines) of the
+    angles position * base^(-2i/rot_dim), computed in binary64."""
+    inv = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def rotate_quantise(x, positions=None, table=None, interleaved=False, out=None, status=None, stream=None):
+    """Rotated rows in the indexer's FP8 form: x [S, H, D] bf16 or fp16 ->
+    (codes [S, H, D] uint8, scale [S, H] float32), to be passed to `topk` as q
+    and q_scale (with H = 1, as k and k_scale rows).
+
+    positions [S] int32 (None: 0, 1, ...), table as from `rope_table` (None: no
+    rotation).  out = (codes, scale) writes into given contiguous tensors, e.g.
+    the next rows of the indexer's key arrays.
+    """
+    act = _act(x, "x")
+    stride = _tokens(x, "x", x.device)
+    S, H, D = x.shape
+    rot = _rotation(table, interleaved, x.device)
+    pos = None if positions is None else _ints(positions, "positions", x.device, (S,))
+    with _On(x.device, stream) as cs:
+        if out is None:
+            out = (torch.empty((S, H, D), dtype=torch.uint8, device=x.device),
+                   torch.empty((S, H), dtype=torch.float32, device=x.device))
+        codes, scale = out
+        _need(codes.dtype in (torch.uint8, torch.float8_e4m3fn) and codes.is_contiguous() and codes.numel() == S * H * D
+              and codes.device == x.device and scale.dtype == torch.float32 and scale.is_contiguous()
+              and scale.numel() == S * H and scale.device == x.device,
+              "out must be contiguous codes (S*H*D uint8) and scales (S*H float32) on x's device")
+        _check("indexer_rotate_quantise", _lib.indexer_rotate_quantise(
+            x.data_ptr(), S, H, D, act, stride, pos, rot, codes.data_ptr(), scale.data_ptr(),
+            None if status is None else _ints(status, "status", x.device, (1,)), cs))
+    return codes, scale
+
+
+class KVCache(NamedTuple):
+    """A paged 8-bit cache: k and v [pages, page_size, heads, D] e4m3 codes
+    (uint8 or float8_e4m3fn; any strides that both share and that keep a head's D
+    codes together, so [pages, heads, page_size, D] memory can be given
+    transposed), k_scale and v_scale [pages, page_size // block, heads] float32."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def descriptor(self) -> CacheDesc:
+        k, v, ks, vs = self
+        _need(k.dim() == 4 and v.shape == k.shape and v.stride() == k.stride() and k.stride(3) == 1
+              and k.dtype in (torch.uint8, torch.float8_e4m3fn) and v.dtype == k.dtype and v.device == k.device,
+              "k and v must be alike: [pages, page_size, heads, D] e4m3 codes, the last dimension contiguous")
+        pages, page_size, heads, D = k.shape
+        _need(ks.dim() == 3 and ks.shape == vs.shape and ks.shape[0] == pages and ks.shape[2] == heads
+              and 0 < ks.shape[1] <= page_size and page_size % ks.shape[1] == 0
+              and ks.dtype == vs.dtype == torch.float32 and ks.is_contiguous() and vs.is_contiguous()
+              and ks.device == vs.device == k.device,
+              "k_scale and v_scale must be contiguous [pages, page_size // block, heads] float32 tensors")
+        sp, st, sh, _ = k.stride()
+        return CacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, sp, st, sh,
+                         page_size, page_size // ks.shape[1], heads, D)
+
+
+def allocate_cache(pages, page_size, heads, D, block=16, device="cuda") -> KVCache:
+    """A cache for pages * page_size tokens, uninitialised (what a sequence has
+    not been given by `cache_append` is never read)."""
+    _need(block >= 1 and page_size % block == 0, "page_size must be a multiple of block")
+    k, v = (torch.empty((pages, page_size, heads, D), dtype=torch.uint8, device=device) for _ in range(2))
+    ks, vs = (torch.empty((pages, page_size // block, heads), dtype=torch.float32, device=device) for _ in range(2))
+    return KVCache(k, v, ks, vs)
+
+
+def _sequences(S, cu_q, kv_len, page_table, device) -> Sequences:
+    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
+    _need(page_table.dim() == 2 and page_table.shape[0] == B and page_table.dtype == torch.int32
+          and page_table.device == device and (page_table.numel() == 0 or page_table.stride(1) == 1
+                                               or page_table.shape[1] == 1),
+          f"page_table must be a [{B}, pages] int32 tensor on {device} with contiguous rows")
+    return Sequences(S, _ints(cu_q, "cu_q", device, (B + 1,)), _ints(kv_len, "kv_len", device, (B,)),
+                     page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]) if B > 1 else
+                     page_table.shape[1], page_table.shape[1], B)
+
+
+def cache_append(cache: KVCache, k, v, cu_q, kv_len, page_table, table=None, interleaved=False, q=None, q_out=None,
+                 status=None, stream=None):
+    """Appends the rows of k and v [S, heads, D] (bf16 or fp16) to the cache, k
+    rotated by its position on the way, quantised with a power-of-two scale per
+    block of tokens and head.
+
+    Rows cu_q[b] .. cu_q[b+1]-1 are the newest tokens of sequence b, whose
+    length with them is kv_len[b]; its position p lies at offset p % page_size of
+    page page_table[b, p // page_size].  With q [S, Hq, D] given, its rotated
+    rows are returned (in q_out, if given); rows that belong to no sequence are
+    left as they were.  status: a [1] int32 tensor that bits are ORed into.
+    """
+    device = cache.k.device
+    desc = cache.descriptor()
+    S = k.shape[0]
+    act = _act(k, "k")
+    stride = _tokens(k, "k", device, (S, desc.heads, desc.D))
+    _need(_tokens(v, "v", device, (S, desc.heads, desc.D), k.dtype) == stride, "k and v must have the same strides")
+    seqs = _sequences(S, cu_q, kv_len, page_table, device)
+    rot = _rotation(table, interleaved, device)
+    q_heads = q_stride = 0
+    with _On(device, stream) as cs:
+        if q is not None:
+            q_heads = q.shape[1]
+            q_stride = _tokens(q, "q", device, (S, q_heads, desc.D), k.dtype)
+            if q_out is None:
+                q_out = torch.empty((S, q_heads, desc.D), dtype=q.dtype, device=device)
+            _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.device == device
+                  and q_out.is_contiguous(), "q_out must be contiguous and like q")
+        else:
+            _need(q_out is None, "q_out without q")
+        _check("indexer_cache_append", _lib.indexer_cache_append(
+            desc, seqs, k.data_ptr(), v.data_ptr(), stride, act, rot, None if q is None else q.data_ptr(), q_heads,
+            q_stride, None if q_out is None else q_out.data_ptr(),
+            None if status is None else _ints(status, "status", device, (1,)), cs))
+    return q_out
+
+
+def cache_attend(cache: KVCache, q, cu_q, kv_len, page_table, scale=None, causal=True, selected=None, max_q=0,
+                 with_lse=False, out=None, workspace=None, status=None, stream=None):
+    """Attention of q [S, Hq, D] (bf16 or fp16, already rotated) over the cache:
+    out [S, Hq, D], and with_lse=True also the log-sum-exp [S, Hq] float32.
+
+    Sequences as in `cache_append` (kv_len counts the newest rows, already
+    appended).  A row sees its sequence's positions up to its own, or with
+    causal=False all of them; selected = (idx [S, W], len [S]) int32, as `topk`
+    returns them for positions counted from the sequence's start, narrows that to
+    the positions named.  A row that sees nothing gives 0 and -inf.  scale
+    defaults to D ** -0.5.  max_q: rows of the longest sequence, if known (a
+    speed hint).  workspace: a uint8 tensor kept by the caller (its size from
+    `cache_attend_workspace_bytes`); by default it is allocated for the call.
+    """
+    device = cache.k.device
+    desc = cache.descriptor()
+    act = _act(q, "q")
+    S, Hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
+    stride = _tokens(q, "q", device, (S, Hq, desc.D))
+    seqs = _sequences(S, cu_q, kv_len, page_table, device)
+    si = sl = None
+    width = 0
+    if selected is not None:
+        idx, lens = selected
+        _need(idx.dim() == 2 and idx.shape[1] > 0, "selected indices must be [S, W] with W > 0")
+        width = idx.shape[1]
+        si, sl = _ints(idx, "selected indices", device, (S, width)), _ints(lens, "selected lengths", device, (S,))
+    att = Attention(Hq, act, 1 if causal else 0, width, max_q, scale if scale is not None else 1 / math.sqrt(desc.D))
+    with _On(device, stream) as cs:
+        n = ctypes.c_size_t()
+        _check("indexer_cache_attend_workspace_bytes",
+               _lib.indexer_cache_attend_workspace_bytes(desc, seqs, att, n))
+        if workspace is None:
+            workspace = torch.empty((n.value,), dtype=torch.uint8, device=device)
+        _need(workspace.device == device and workspace.is_contiguous(), f"workspace must be contiguous on {device}")
+        if out is None:
+            out = torch.empty((S, Hq, desc.D), dtype=q.dtype, device=device)
+        _need(out.shape == q.shape and out.dtype == q.dtype and out.device == device and out.is_contiguous(),
+              "out must be contiguous and like q")
+        lse = torch.empty((S, Hq), dtype=torch.float32, device=device) if with_lse else None
+        _check("indexer_cache_attend", _lib.indexer_cache_attend(
+            desc, seqs, att, q.data_ptr(), stride, si, sl, out.data_ptr(), None if lse is None else lse.data_ptr(),
+            None if status is None else _ints(status, "status", device, (1,)), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), cs))
+    return (out, lse) if with_lse else out
+
+
+def cache_attend_workspace_bytes(cache: KVCache, q, cu_q, kv_len, page_table, selected_width=0) -> int:
+    """Bytes of workspace for `cache_attend` on these tensors' shapes."""
+    desc = cache.descriptor()
+    seqs = _sequences(q.shape[0], cu_q, kv_len, page_table, cache.k.device)
+    n = ctypes.c_size_t()
+    with _On(cache.k.device, None):
+        _check("indexer_cache_attend_workspace_bytes", _lib.indexer_cache_attend_workspace_bytes(
+            desc, seqs, Attention(q.shape[1], _act(q, "q"), 1, selected_width, 0, 1.0), n))
+    return n.value

@@ -352,12 +352,158 @@ indexer_status indexer_pair_regions(const int32_t* idx, const int32_t* len,
                                     int32_t* out_right, int32_t* out_counts,
                                     void* stream);
 
+/* ------------------------------------------------------------------------
+ * Around the indexer in a serving step: its FP8 rows are made from 16-bit
+ * projections (indexer_rotate_quantise), the keys and values of new tokens
+ * go to a paged 8-bit cache (indexer_cache_append), and the queries attend
+ * over the cached tokens (indexer_cache_attend): over all of a sequence, or
+ * over the positions that out_idx / out_len of the indexer name.
+ * ------------------------------------------------------------------------ */
+
+/* Element type of activations (x, k, v, q, out below). */
+typedef enum { INDEXER_ACT_BF16 = 0, INDEXER_ACT_FP16 = 1 } indexer_act;
+
+/* Position rotation of the first `rot_dim` dimensions of a head.  Row p of
+ * `table` holds rot_dim/2 cosines, then rot_dim/2 sines, of the angles of
+ * position p.  Dimension pair i is (i, i + rot_dim/2), or (2i, 2i+1) when
+ * `interleaved`:  (a, b) -> (a cos - b sin, b cos + a sin), in FP32 with each
+ * product and the difference or sum rounded on its own.  rot_dim = 0 rotates
+ * nothing; otherwise a multiple of 16, at most D. */
+typedef struct {
+  const float* table;   /* [rows, rot_dim] DEVICE, 16-byte aligned; NULL when rot_dim = 0 */
+  int64_t rows;
+  int32_t rot_dim;
+  int32_t interleaved;  /* 0 or 1 */
+} indexer_rotation;
+
+/* Rotated rows in the indexer's FP8 form (dtype INDEXER_FP8_E4M3): for every
+ * row (t, h) of x, y = rotation of x at positions[t], then
+ *   scale[t, h] = amax |y| / 448 (1 for a zero row),
+ *   codes[t, h, :] = RNE_e4m3(y / scale).
+ *   x         [S, H, D] activations, 16-byte aligned, tokens `x_stride`
+ *             elements apart (a multiple of 8, at least H*D; H and D packed),
+ *             so a slice of a wider projection can be given
+ *   positions [S] int32 DEVICE, or NULL for 0, 1, ...; a position outside the
+ *             table makes the token's codes NaN (0x7F) and its scales 1 and
+ *             sets bit 3 of *status.  Not read when rot_dim = 0.
+ *   codes     [S, H, D] uint8, 8-byte aligned; scale [S, H] float32
+ *   status    int32 DEVICE word that bits are ORed into, or NULL
+ * NaN and infinite inputs give NaN codes in their row.  D is 64 or 128.
+ * With H = 1 and codes / scale pointing at row T of the indexer's key arrays
+ * this appends index keys. */
+indexer_status indexer_rotate_quantise(const void* x, int64_t S, int32_t H, int32_t D, int32_t act,
+                                       int64_t x_stride, const int32_t* positions,
+                                       const indexer_rotation* rotation, uint8_t* codes, float* scale,
+                                       int32_t* status, void* stream);
+
+/* A paged cache of keys and values in e4m3 codes.  The token at offset o of
+ * page p has its head h at byte p*page_stride + o*token_stride + h*head_stride
+ * of k and of v (both have the same strides, multiples of 16; a head's D codes
+ * are contiguous), and stands for code * scale with
+ *   scale = k_scale[p, o / block, h]  (v_scale for values),
+ * both [n_pages, page_size/block, heads] float32, positive and finite. */
+typedef struct {
+  uint8_t* k;            /* DEVICE, 16-byte aligned */
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t n_pages;
+  int64_t page_stride;   /* bytes; n_pages * page_stride at most 2^36 */
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t page_size;     /* tokens a page, a multiple of block, at most 2^20 */
+  int32_t block;         /* tokens that share a scale: a power of two, 1..128 */
+  int32_t heads;         /* key/value heads, at most 1024 */
+  int32_t D;             /* 64 or 128 */
+} indexer_cache;
+
+/* The sequences of a call.  Rows cu_q[b] .. cu_q[b+1]-1 of the activations
+ * are the newest tokens of sequence b, whose length with them is kv_len[b]:
+ * row r has position kv_len[b] - (cu_q[b+1] - r).  Position p of sequence b is
+ * at offset p % page_size of page page_table[b, p / page_size].  Rows from
+ * cu_q[B] on belong to no sequence and are neither read nor written. */
+typedef struct {
+  int64_t S;                  /* rows of the activations (S times heads < 2^31) */
+  const int32_t* cu_q;        /* [B+1] DEVICE, rising from 0 */
+  const int32_t* kv_len;      /* [B] DEVICE */
+  const int32_t* page_table;  /* [B, table_pages] DEVICE */
+  int64_t table_stride;       /* entries between rows of page_table */
+  int32_t table_pages;
+  int32_t B;                  /* at most 2^20 */
+} indexer_sequences;
+
+/* Appends the rows k and v of every sequence to the cache, k (and q, when
+ * given) rotated by its position on the way.
+ *   k, v      [S, heads, D] activations, tokens kv_stride elements apart
+ *   q, q_out  [S, Hq, D] activations, q tokens q_stride elements apart, q_out
+ *             contiguous; both NULL for none
+ * Strides are multiples of 8 elements, pointers 16-byte aligned.
+ * A block's scale is the least power of two s with amax <= 448 s, no less
+ * than 2^-100, over the block's tokens (per head, for keys and values each):
+ * powers of two keep every code's relative precision and make the change of
+ * a block's scale exact except for codes that fall below 2^-6.  Where a
+ * sequence's first new token lies inside a block, that block's earlier tokens
+ * keep its scale as a lower bound; if it rises their codes become
+ * RNE_e4m3(code * old / new).  A block whose first token is new starts
+ * anew, whatever it held.  Appending the same tokens again leaves the cache
+ * as it is, and splitting an append at any token gives the same scales.
+ * NaN and infinite values become NaN codes and do not count for the scale.
+ * No two sequences may write to the same page.  A token whose page lies
+ * outside [0, n_pages) or beyond table_pages, or whose position is negative
+ * or outside the rotation table, is skipped (for the last two its q row too)
+ * and bit 3 of *status is set. */
+indexer_status indexer_cache_append(const indexer_cache* cache, const indexer_sequences* seqs,
+                                    const void* k, const void* v, int64_t kv_stride, int32_t act,
+                                    const indexer_rotation* rotation, const void* q, int32_t Hq,
+                                    int64_t q_stride, void* q_out, int32_t* status, void* stream);
+
+/* Attention over the cache:
+ *   out[r, a, :] = sum_j p_j v_j,  p = softmax_j(scale * q[r, a, :] . k_j),
+ * head a reading key/value head a / (Hq/heads), j over the positions below
+ * kv_len[b] that row r sees: all of them, or with `causal` those up to its
+ * own, and with sel_width > 0 only those that sel_idx[r, 0 .. sel_len[r])
+ * names (each as often as it is named; entries that are negative or not seen
+ * are passed over).  out_idx / out_len of indexer_topk are such a selection
+ * when their positions count from the sequence's start; for compressed keys
+ * use a cache of compressed keys and causal = 0.  A row that sees nothing
+ * gives 0, and lse -infinity.  lse = log sum_j exp(scale * q . k_j).
+ * Tokens whose page lies outside the cache or the page table are not seen
+ * and set bit 3 of *status.  What the cache holds elsewhere than at seen
+ * positions never matters.
+ * Scores, softmax statistics and sums are FP32; the probabilities are
+ * rounded to FP16 (relative to the largest seen, with 2^-31 of it as the least),
+ * as a factor of the value products only.  The value scales
+ * of one sequence may span a factor of 2^120. */
+typedef struct {
+  int32_t Hq;         /* query heads: a multiple of the cache's heads, at most 128 times as many */
+  int32_t act;        /* indexer_act of q and out */
+  int32_t causal;     /* 0 or 1 */
+  int32_t sel_width;  /* 0: no selection */
+  int32_t max_q;      /* rows of the longest sequence, or 0 if unknown (a speed hint only) */
+  float scale;        /* finite */
+} indexer_attention;
+
+/* Workspace of indexer_cache_attend: scratch between calls, no
+ * initialisation; calls that may overlap on the GPU need one each. */
+indexer_status indexer_cache_attend_workspace_bytes(const indexer_cache* cache, const indexer_sequences* seqs,
+                                                    const indexer_attention* attention, size_t* bytes);
+
+/*   q [S, Hq, D], tokens q_stride elements apart (a multiple of 8); out
+ *   [S, Hq, D] contiguous; lse [S, Hq] float32 or NULL; sel_idx
+ *   [S, sel_width] and sel_len [S] int32, NULL without a selection. */
+indexer_status indexer_cache_attend(const indexer_cache* cache, const indexer_sequences* seqs,
+                                    const indexer_attention* attention, const void* q, int64_t q_stride,
+                                    const int32_t* sel_idx, const int32_t* sel_len, void* out, float* lse,
+                                    int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then reads the device status word that indexer_topk
  * keeps in `workspace` (0 = no fault).  Bit 0: a pipeline wait in the kernel
  * gave up after its time limit (the result is not valid); bit 1: a candidate
  * buffer would have overflowed (never expected; the result is not valid);
  * bit 2: a seed threshold of indexer_topk_witness was above some query's
- * K-th score (never expected; that row may be short).
+ * K-th score (never expected; that row may be short).  With the status word
+ * of the cache calls as `workspace`, bit 3: a token's page or position does
+ * not exist.
  * Also clears the word.  Host pointer `flags`. */
 indexer_status indexer_read_status(void* workspace, int32_t* flags, void* stream);
 
