@@ -123,31 +123,57 @@ struct TokenEntry {
 };
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;
 
-__device__ __forceinline__ TokenEntry translate(const AttendParams& p, const Tile& x, int h, int e) {
-  TokenEntry t;
-  t.off16 = kNoToken;
-  t.pos = INT32_MAX;
-  t.ks = 0.f;
-  t.lvs = 0.f;
-  if (e >= x.n_keys) return t;
-  int pos = e;
-  if (p.sel_width) {
-    pos = __ldg(p.sel_idx + static_cast<int64_t>(x.row) * p.sel_width + e);
-    if (pos < 0 || pos >= min(x.len, row_limit(p, x, x.first))) return t;
+// Translation of a key entry of (tile, head) to its token in three dependent
+// loads, so that a caller can issue each well before its value is used.  An
+// entry at or beyond `end`, or that stands for nothing, is pos INT_MAX throughout.
+struct Translate {
+  const AttendParams& p;
+  const Tile& x;
+  int h, end, seen;
+  const int32_t* sel;
+  const int32_t* pages;
+
+  struct Index { int pos; };                              // position, or INT_MAX
+  struct Page { int pos; int off; int page; };            // page: as loaded
+  struct Scale { int pos; uint32_t off16; float ks, vs; };
+
+  __device__ __forceinline__ Translate(const AttendParams& p_, const Tile& x_, int h_, int end_)
+      : p(p_), x(x_), h(h_), end(end_) {
+    sel = p.sel_width ? p.sel_idx + static_cast<int64_t>(x.row) * p.sel_width : nullptr;
+    pages = p.s.pages + x.b * p.s.page_stride;
+    seen = p.sel_width ? min(min(x.len, row_limit(p, x, x.first)), INT32_MAX) : 0;
   }
-  int off;
-  const int64_t page = page_of(p.s, p.c, x.b, pos, &off);
-  if (page < 0) {
-    if (p.status) atomicOr(p.status, kStatusToken);
-    return t;
+  __device__ __forceinline__ Index index(int e) const {
+    if (e >= end || e < 0) return Index{INT32_MAX};
+    return Index{sel ? __ldg(sel + e) : e};
   }
-  const int64_t si = (page * p.c.page_blocks + (off >> p.c.block_shift)) * p.c.heads + h;
-  t.off16 = static_cast<uint32_t>(page * p.c.page16 + off * p.c.token16);
-  t.pos = pos;
-  t.ks = __ldg(p.c.ks + si);
-  t.lvs = __log2f(fmaxf(__ldg(p.c.vs + si), kMinBlockScale));
-  return t;
-}
+  __device__ __forceinline__ Page page(const Index& i) const {
+    Page r{INT32_MAX, 0, 0};
+    if (i.pos == INT32_MAX || (sel && (i.pos < 0 || i.pos >= seen))) return r;
+    const int pi = i.pos / p.c.page_size;
+    r.pos = i.pos;
+    r.off = i.pos - pi * p.c.page_size;
+    r.page = pi < p.s.table_pages ? __ldg(pages + pi) : -1;
+    return r;
+  }
+  __device__ __forceinline__ Scale scale(const Page& g) const {
+    Scale r{INT32_MAX, kNoToken, 0.f, 1.f};
+    if (g.pos == INT32_MAX) return r;
+    if (g.page < 0 || g.page >= p.c.n_pages) {
+      if (p.status) atomicOr(p.status, kStatusToken);
+      return r;
+    }
+    const int64_t si = (static_cast<int64_t>(g.page) * p.c.page_blocks + (g.off >> p.c.block_shift)) * p.c.heads + h;
+    r.pos = g.pos;
+    r.off16 = static_cast<uint32_t>(g.page * p.c.page16 + g.off * p.c.token16);
+    r.ks = __ldg(p.c.ks + si);
+    r.vs = __ldg(p.c.vs + si);
+    return r;
+  }
+  __device__ __forceinline__ TokenEntry entry(const Scale& s) const {
+    return TokenEntry{s.off16, s.pos, s.ks, __log2f(fmaxf(s.vs, kMinBlockScale))};
+  }
+};
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -198,11 +224,11 @@ __device__ __forceinline__ int block_scan_tiles(int v, int* total, int* warp_sum
   return before + inc - v;
 }
 
-cudaError_t launch_attend_stream(const AttendParams& p, int D, bool f16, int grid, cudaStream_t stream);
-cudaError_t launch_attend_join(const AttendParams& p, int D, int R, bool f16, cudaStream_t stream);
-int attend_stream_ctas_per_sm(int D);
+// rows: of a tile, 8 or 16
+cudaError_t launch_attend_stream(const AttendParams& p, int D, int rows, bool f16, int grid, cudaStream_t stream);
+cudaError_t launch_attend_join(const AttendParams& p, int D, int rows, bool f16, cudaStream_t stream);
+int attend_stream_ctas_per_sm(int rows);
 
-constexpr int kStreamRows = 16;    // rows of a tile of the streaming kernel
-constexpr int kMaxSplitTiles = 512;  // tiles of a launch whose CTAs share units
+constexpr int kMaxSplitTiles = 255;  // tiles of a launch whose CTAs share units
 
 }  // namespace hwr

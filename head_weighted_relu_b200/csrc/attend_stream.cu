@@ -1,17 +1,23 @@
 // attend_stream.cu -- attention over the 8-bit cache for few query rows per
-// key/value head (decode steps, selected positions): up to 16 rows share one
-// pass over the keys, which is bound by reading them.
+// key/value head (decode steps, selected positions): up to 8 or 16 rows share
+// one pass over the keys, which is bound by reading them.
 //
 // A warp works alone: it copies 16 tokens' codes (2 D bytes each) at a time
-// into a ring of its own in shared memory (cp.async, kDepth steps ahead), so
-// that nothing but its own copies holds it up.  Codes become FP16 in registers
-// (exact) in the fragment layout of mma.m16n8k16 without any shuffle: the order
-// of the head dimension inside a product is free, so lane group c takes
-// dimensions 32c .. 32c+31 of a key row as two 16-byte reads; and the order of
-// an output's columns is free, so lane group g takes columns 16g .. 16g+15 of
-// four value rows as four 16-byte reads, interleaved by byte permutes.  The
-// score fragment is the weight fragment of the second product.  A CTA's four
+// into a ring of its own in shared memory (cp.async, kDepth - 1 steps ahead),
+// and translates key entries to cache tokens two steps at a time, each of the
+// dependent loads (selected index -> page -> scales) issued one pair of steps
+// before its value is used; no barrier stands in the key loop.  A CTA's four
 // warps take every fourth 16 tokens of its keys and join at the end.
+//
+// Both products are taken transposed, tokens or value columns on the 16 rows of
+// mma.m16n8k16 and query rows on its 8 columns, so that 8 rows (one query of 8
+// heads) waste nothing.  Codes become FP16 in registers (exact) in fragment
+// order without a shuffle: the order of the head dimension inside a product is
+// free, so lane group c takes dimensions (D/4)c .. of a key row as 16-byte
+// reads; and which columns a tile of the second product holds is free, so lane
+// group g takes columns (D/8)g .. of four value rows as 16-byte reads,
+// interleaved by byte permutes.  The weights pass to the second product
+// through a register transpose (movmatrix).
 #include "attend.cuh"
 
 namespace hwr {
@@ -20,17 +26,18 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStep = 16;                  // tokens of a warp step
 constexpr int kUnit = kWarps * kStep;      // keys of a unit
-constexpr int kChunk = 256;                // keys translated at a time
 constexpr int kDepth = 3;                  // ring entries per warp
-constexpr int kChunkSteps = kChunk / kUnit;
+constexpr int kTableSteps = 4;             // steps whose translation is kept
 
-template <int D>
+template <int D, int NT>
 struct Smem {
+  static constexpr int kRows = 8 * NT;
   static constexpr int kStepBytes = 2 * kStep * D;
   static constexpr int kRing = kWarps * kDepth * kStepBytes;
-  static constexpr int kJoin = kWarps * kStreamRows * (D + 4) * 4;   // reuses the ring
-  static constexpr int kTable = 2 * kChunk * 16;
-  static constexpr int kBytes = (kRing > kJoin ? kRing : kJoin) + kTable + kWarps * kStreamRows * 8;
+  static constexpr int kJoin = kWarps * kRows * (D + 4) * 4;   // reuses the ring
+  static constexpr int kData = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kTable = kWarps * kTableSteps * kStep * 16;
+  static constexpr int kBytes = kData + kTable + kWarps * kRows * 8;
 };
 
 // Offset of 16-byte chunk `ch` of token row `r` in a step's K or V image: rows
@@ -62,25 +69,33 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// 8x8 transpose of 16-bit values held as a lane's row lane/4, columns 2(lane%4), +1.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w)); }
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16)); }
 
-// The query fragments of rows g and g+8: dimensions 4 steps at a time, of the
-// lane's own D/4 consecutive ones.  Returns the two rows' score factors.
-template <int D, bool F16>
-__device__ __forceinline__ void load_q(const AttendParams& p, const Tile& x, int h, uint32_t (&qf)[D / 16][4],
-                                       float (&factor)[2]) {
+// Query fragments: row g of each 8, the lane's own D/4 consecutive dimensions,
+// 4 per product step.  factor: what the accumulated product of rows 2c, 2c+1 is
+// multiplied by.
+template <int D, int NT, bool F16>
+__device__ __forceinline__ void load_q(const AttendParams& p, const Tile& x, int h, uint32_t (&qf)[D / 16][NT][2],
+                                       float (&factor)[NT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int i = g + 8 * half;
+  for (int nt = 0; nt < NT; ++nt) {
+    const int i = g + 8 * nt;
     const bool on = i < x.rows;
     const int pair = x.first + (on ? i : 0);
-    const uint8_t* src =
-        p.q + (x.q0 + pair / p.G) * p.q_stride + (h * p.G + pair % p.G) * (2 * D) + c * (D / 2);
+    const uint8_t* src = p.q + (x.q0 + pair / p.G) * p.q_stride + (h * p.G + pair % p.G) * (2 * D) + c * (D / 2);
     uint32_t w[D / 8];
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) {
@@ -105,25 +120,27 @@ __device__ __forceinline__ void load_q(const AttendParams& p, const Tile& x, int
         w[k] = half2_of(f.x * inv, f.y * inv);
       }
     }
-    factor[half] = s * p.scale_log2;
+    s *= p.scale_log2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) factor[nt][j] = __shfl_sync(kFullMask, s, (2 * c + j) * 4);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      qf[k][half] = w[2 * k];          // dimensions 4k, 4k+1 of the lane's
-      qf[k][half + 2] = w[2 * k + 1];  // 4k+2, 4k+3
+      qf[k][nt][0] = w[2 * k];      // dimensions 4k, 4k+1 of the lane's
+      qf[k][nt][1] = w[2 * k + 1];  // 4k+2, 4k+3
     }
   }
 }
 
 template <int D>
-__device__ __forceinline__ void issue_step(const AttendParams& p, const TokenEntry* table, int step_in_table,
-                                           int64_t head, uint32_t ring) {
+__device__ __forceinline__ void issue_step(const AttendParams& p, const TokenEntry* table, int64_t head,
+                                           uint32_t ring) {
   // 16 rows of D/16 chunks, of K and of V
   const int lane = threadIdx.x & 31;
   constexpr int kCh = D / 16, kPer = kCh * kStep / 32;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int r = (i * 32 + lane) / kCh, ch = lane % kCh;
-    const uint32_t off = table[step_in_table * kStep + r].off16;
+    const uint32_t off = table[r].off16;
     const bool on = off != kNoToken;
     const int64_t at = on ? (static_cast<int64_t>(off) + head + ch) * 16 : 0;
     const uint32_t dst = ring + chunk_at<D>(r, ch);
@@ -133,25 +150,69 @@ __device__ __forceinline__ void issue_step(const AttendParams& p, const TokenEnt
   cp_async_commit();
 }
 
+// 0xFF in each byte of w that is a NaN code (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
+
+// Takes the NaN codes out of a step's values, and makes NaN the outputs of the
+// rows that do see them: the columns where (code is NaN) x (row sees token),
+// again a matrix product, is not zero.  sc: the masked scores.
+template <int D, int NT>
+__device__ __forceinline__ void poison(const float (&sc)[NT][4], uint32_t (&vw)[4][D / 32],
+                                       float (&acc)[D / 16][NT][4]) {
+  uint32_t sees[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      sees[nt][t] = transpose8x8((sc[nt][2 * t] == -INFINITY ? 0u : 0x3C00u) |
+                                 (sc[nt][2 * t + 1] == -INFINITY ? 0u : 0x3C000000u));
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    uint32_t nb[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      nb[t] = nan_bytes(vw[t][k]);
+      vw[t][k] &= ~nb[t];
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t a[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int sh = 16 * half + 8 * (e & 1), t = e & 2;
+        a[e] = ((nb[t] >> sh) & 1u) * 0x3C00u | ((nb[t + 1] >> sh) & 1u) * 0x3C000000u;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float hit[4] = {};
+        mma16816(hit, a, sees[nt][0], sees[nt][1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (hit[e] > 0.f) acc[2 * k + half][nt][e] = NAN;
+      }
+    }
+  }
+}
+
 // Writes the joined rows of a segment: whole ones as outputs, others as parts.
-template <int D, bool F16>
+template <int D, int NT, bool F16>
 __device__ __forceinline__ void store_rows(const AttendParams& p, const Tile& x, int h, bool whole, int64_t part,
                                            const float* acc, const float2* ml) {
-  // acc [kWarps][16][D+4] (columns in order), ml [kWarps][16]
-  constexpr int kPer = D / 8;  // threads of a row
+  // acc [kWarps][rows][D+4] (columns in order), ml [kWarps][rows]
+  constexpr int R = 8 * NT, kPer = D / 8;  // threads of a row
   const int d = (threadIdx.x % kPer) * 8;
   for (int i = threadIdx.x / kPer; i < x.rows; i += kWarps * 32 / kPer) {
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kStreamRows + i].x);
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * R + i].x);
     float l = 0.f, o[8] = {};
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 v = ml[w * kStreamRows + i];
+      const float2 v = ml[w * R + i];
       const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
       l += f * v.y;
       if (f != 0.f) {
-        const float* a = acc + (w * kStreamRows + i) * (D + 4) + d;
+        const float* a = acc + (w * R + i) * (D + 4) + d;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += f * a[e];
       }
@@ -166,184 +227,152 @@ __device__ __forceinline__ void store_rows(const AttendParams& p, const Tile& x,
       *reinterpret_cast<uint4*>(p.out + (at * D + d) * 2) = v;
       if (p.lse && d == 0) p.lse[at] = m == -INFINITY ? -INFINITY : kLn2 * (m - kHead + log2f(l));
     } else {
-      float* dst = p.part_o + (part * kStreamRows + i) * D + d;
+      float* dst = p.part_o + (part * R + i) * D + d;
       *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
       *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
-      if (d == 0) p.part_ml[part * kStreamRows + i] = make_float2(m, l);
-    }
-  }
-}
-
-// 0xFF in each byte of w that is a NaN code (0x7F or 0xFF).
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
-
-// Takes the NaN codes out of a step's values, and makes NaN the outputs of the
-// rows that do see them: the columns where (row sees token) x (code is NaN),
-// again a matrix product, is not zero.  sc: the masked scores.
-template <int D>
-__device__ __forceinline__ void poison(const float (&sc)[2][4], uint32_t (&vw)[4][D / 32], float (&acc)[D / 8][4]) {
-  uint32_t sees[4];
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-      sees[nt * 2 + half] = (sc[nt][half * 2] == -INFINITY ? 0u : 0x3C00u) |
-                            (sc[nt][half * 2 + 1] == -INFINITY ? 0u : 0x3C000000u);
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) {
-    uint32_t nb[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      nb[t] = nan_bytes(vw[t][k]);
-      vw[t][k] &= ~nb[t];
-    }
-#pragma unroll
-    for (int byte = 0; byte < 4; ++byte) {
-      const int sh = 8 * byte;
-      float hit[4] = {};
-      mma16816(hit, sees, ((nb[0] >> sh) & 1u) * 0x3C00u | ((nb[1] >> sh) & 1u) * 0x3C000000u,
-               ((nb[2] >> sh) & 1u) * 0x3C00u | ((nb[3] >> sh) & 1u) * 0x3C000000u);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (hit[e] > 0.f) acc[4 * k + byte][e] = NAN;
+      if (d == 0) p.part_ml[part * R + i] = make_float2(m, l);
     }
   }
 }
 
 // Keys [64 u0, 64 u1) of (tile, head).
-template <int D, bool F16>
+template <int D, int NT, bool F16>
 __device__ void segment(const AttendParams& p, const Tile& x, int h, int u0, int u1, bool whole, int64_t part,
                         uint8_t* smem) {
-  constexpr int kRingBytes = Smem<D>::kRing > Smem<D>::kJoin ? Smem<D>::kRing : Smem<D>::kJoin;
-  TokenEntry* table = reinterpret_cast<TokenEntry*>(smem + kRingBytes);
-  float2* ml = reinterpret_cast<float2*>(smem + kRingBytes + Smem<D>::kTable);
+  using L = Smem<D, NT>;
+  constexpr int R = L::kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const uint32_t ring = smem_u32(smem) + warp * (kDepth * Smem<D>::kStepBytes);
+  TokenEntry* table = reinterpret_cast<TokenEntry*>(smem + L::kData) + warp * (kTableSteps * kStep);
+  float2* ml = reinterpret_cast<float2*>(smem + L::kData + L::kTable);
+  const uint32_t ring = smem_u32(smem) + warp * (kDepth * L::kStepBytes);
   const int64_t head = h * p.c.head16;
-  const int n = u1 - u0;
+  const int n = u1 - u0;  // steps of this warp
 
-  // translate chunk 0 (and 1 before it is needed)
-  auto fill = [&](int chunk) {
-    TokenEntry* t = table + (chunk & 1) * kChunk;
-#pragma unroll
-    for (int i = 0; i < kChunk / (kWarps * 32); ++i) {
-      const int k = i * kWarps * 32 + threadIdx.x;
-      t[k] = translate(p, x, h, u0 * kUnit + chunk * kChunk + k);
-    }
-  };
   __syncthreads();  // the previous segment's buffers are free
-  fill(0);
-  uint32_t qf[D / 16][4];
-  float factor[2];
-  load_q<D, F16>(p, x, h, qf, factor);
-  int limit[2];
+
+  // The lane's entry of a pair of steps: token lane%16 of step 2*pair + lane/16.
+  const int e0 = u0 * kUnit + (lane >> 4) * kUnit + warp * kStep + (lane & 15);
+  auto entry = [&](int pair) { return e0 + pair * 2 * kUnit; };
+  const int end = min(x.n_keys, u1 * kUnit);
+  Translate tr(p, x, h, end);
+  Translate::Index i0 = tr.index(entry(0)), i1 = tr.index(entry(1)), i2 = tr.index(entry(2)), i3 = tr.index(entry(3));
+  Translate::Page g0 = tr.page(i0), g1 = tr.page(i1), g2 = tr.page(i2);
+  Translate::Scale s0 = tr.scale(g0), s1 = tr.scale(g1);
+  uint32_t qf[D / 16][NT][2];
+  float factor[NT][2];
+  load_q<D, NT, F16>(p, x, h, qf, factor);
+  int limit[NT][2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int i = g + 8 * half;
-    limit[half] = i < x.rows ? row_limit(p, x, x.first + i) : 0;
-  }
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = 8 * nt + 2 * c + j;
+      limit[nt][j] = i < x.rows ? row_limit(p, x, x.first + i) : 0;
+    }
   // the least number of positions that a row of the tile sees
   const int first_limit = p.sel_width ? 0 : row_limit(p, x, x.first);
-  float acc[D / 8][4] = {};
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  __syncthreads();
+  float acc[D / 16][NT][4] = {};
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 
-  int issued = 0;
-  auto step_table = [&](int s) { return ((s / kChunkSteps) & 1) * kChunk + (s % kChunkSteps) * kUnit + warp * kStep; };
-#pragma unroll 1
-  for (; issued < kDepth - 1; ++issued) {
-    if (issued < n && issued < kChunkSteps)
-      issue_step<D>(p, table + step_table(issued), 0, head, ring + issued * Smem<D>::kStepBytes);
+  table[lane] = tr.entry(s0);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) {
+    if (i < n)
+      issue_step<D>(p, table + i * kStep, head, ring + i * L::kStepBytes);
     else
       cp_async_commit();
   }
-  static_assert(kDepth - 1 <= kChunkSteps, "the first chunk covers the first copies");
+  static_assert(kDepth - 1 == 2, "a pair of steps is in flight ahead of the one that is computed");
 
+  int slot = 0;
 #pragma unroll 1
   for (int s = 0; s < n; ++s) {
-    if (s % kChunkSteps == 0) {
-      // the next chunk's table, before a copy of it can be issued; its buffer's
-      // last reader was the step before this one
-      __syncthreads();
-      if (s + kChunkSteps < n) fill(s / kChunkSteps + 1);
-      __syncthreads();
+    if ((s & 1) == 0) {
+      // pair s/2 + 1 into the table; each later pair one load further
+      table[((s + 2) & 3) * kStep + lane] = tr.entry(s1);
+      s1 = tr.scale(g2);
+      g2 = tr.page(i3);
+      i3 = tr.index(entry((s >> 1) + 4));
+      __syncwarp();
     }
-    if (issued < n)
-      issue_step<D>(p, table + step_table(issued), 0, head, ring + (issued % kDepth) * Smem<D>::kStepBytes);
+    const int next = slot >= 1 ? slot - 1 : kDepth - 1;  // the entry of step s - 1, free now: (s + 2) % 3
+    if (s + 2 < n)
+      issue_step<D>(p, table + ((s + 2) & 3) * kStep, head, ring + next * L::kStepBytes);
     else
       cp_async_commit();
-    ++issued;
     cp_async_wait<kDepth - 1>();
     __syncwarp();
-    const uint32_t kb = ring + (s % kDepth) * Smem<D>::kStepBytes, vb = kb + kStep * D;
+    const uint32_t kb = ring + slot * L::kStepBytes, vb = kb + kStep * D;
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
 
-    float sc[2][4] = {};
+    // Scores of tokens g, g+8 (rows) and query rows 2c, 2c+1 (columns), in two
+    // chains of products to halve their latency.
+    float sc[NT][4] = {}, sd[NT][4] = {};
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const int r = nt * 8 + g;
+    for (int i = 0; i < D / 64; ++i) {
+      const uint4 v0 = lds128(kb + chunk_at<D>(g, D == 128 ? 2 * c + i : c));
+      const uint4 v1 = lds128(kb + chunk_at<D>(g + 8, D == 128 ? 2 * c + i : c));
+      const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const uint4 v = lds128(kb + chunk_at<D>(r, D == 128 ? 2 * c + i : c));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a[4] = {cvt_lo(w0[j]), cvt_lo(w1[j]), cvt_hi(w0[j]), cvt_hi(w1[j])};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t b0 = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j]));
-          const uint32_t b1 = e4m3x2_to_f16x2(static_cast<uint16_t>(w[j] >> 16));
-          mma16816(sc[nt], qf[i * 4 + j], b0, b1);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816((j & 1) ? sd[nt] : sc[nt], a, qf[i * 4 + j][nt][0], qf[i * 4 + j][nt][1]);
       }
     }
-    // scores of tokens 2c, 2c+1 (nt 0), 8+2c, 8+2c+1 (nt 1), rows g and g+8
-    const TokenEntry* te = table + step_table(s);
-    float top[2] = {m[0], m[1]};
-    float ivs[4], lvs[4];
+    const TokenEntry* te = table + (s & 3) * kStep;
+    const int4 ea = *reinterpret_cast<const int4*>(te + g), eb = *reinterpret_cast<const int4*>(te + g + 8);
+    const float ks[2] = {__int_as_float(ea.z), __int_as_float(eb.z)};
+    const float lvs[2] = {__int_as_float(ea.w), __int_as_float(eb.w)};
+    const float ivs[2] = {ex2(-lvs[0]), ex2(-lvs[1])};
+    const int pos[2] = {ea.y, eb.y};
+    bool up = false;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int4 e = *reinterpret_cast<const int4*>(te + nt * 8 + 2 * c + j);
-        const float ks = __int_as_float(e.z);
-        lvs[nt * 2 + j] = __int_as_float(e.w);
-        ivs[nt * 2 + j] = ex2(-lvs[nt * 2 + j]);
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float u = fmaf(sc[nt][half * 2 + j] * ks, factor[half], lvs[nt * 2 + j]);
-          u = e.y < limit[half] ? u : -INFINITY;
-          sc[nt][half * 2 + j] = u;
-          top[half] = fmaxf(top[half], u);
+        for (int j = 0; j < 2; ++j) {
+          float u = fmaf((sc[nt][2 * t + j] + sd[nt][2 * t + j]) * ks[t], factor[nt][j], lvs[t]);
+          u = pos[t] < limit[nt][j] ? u : -INFINITY;
+          sc[nt][2 * t + j] = u;
+          up = up || u > m[nt][j] + kSlack;
         }
-      }
-    }
-    // the reference rises only when it is exceeded by the slack, by the row's
-    // maximum over the four lanes that share it
-    const bool up = top[0] > m[0] + kSlack || top[1] > m[1] + kSlack;
+    // A row's reference rises to its largest score when that exceeds it by the slack.
     if (__any_sync(kFullMask, up)) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        top[half] = fmaxf(top[half], __shfl_xor_sync(kFullMask, top[half], 1));
-        top[half] = fmaxf(top[half], __shfl_xor_sync(kFullMask, top[half], 2));
-        const float f = top[half] == m[half] || top[half] == -INFINITY ? 1.f : ex2(m[half] - top[half]);
-        m[half] = top[half];
-        l[half] *= f;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) acc[i][half * 2] *= f, acc[i][half * 2 + 1] *= f;
-      }
+        for (int j = 0; j < 2; ++j) {
+          float top = fmaxf(m[nt][j], fmaxf(sc[nt][j], sc[nt][2 + j]));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+          const float f = top == m[nt][j] ? 1.f : ex2(m[nt][j] - top);
+          m[nt][j] = top;
+          l[nt][j] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) acc[i][nt][j] *= f, acc[i][nt][2 + j] *= f;
+        }
     }
-    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - kHead, m[1] == -INFINITY ? 0.f : m[1] - kHead};
-    uint32_t pf[4];
+    uint32_t pf[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
+    for (int nt = 0; nt < NT; ++nt) {
+      const float r0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kHead;
+      const float r1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kHead;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float p0 = ex2(sc[nt][half * 2] - ref[half]), p1 = ex2(sc[nt][half * 2 + 1] - ref[half]);
-        l[half] = fmaf(p0, ivs[nt * 2], l[half]);
-        l[half] = fmaf(p1, ivs[nt * 2 + 1], l[half]);
-        pf[nt * 2 + half] = half2_of(p0, p1);
+      for (int t = 0; t < 2; ++t) {
+        const float p0 = ex2(sc[nt][2 * t] - r0), p1 = ex2(sc[nt][2 * t + 1] - r1);
+        l[nt][0] = fmaf(p0, ivs[t], l[nt][0]);
+        l[nt][1] = fmaf(p1, ivs[t], l[nt][1]);
+        pf[nt][t] = transpose8x8(half2_of(p0, p1));
       }
     }
     // values: tokens 2c, 2c+1, 2c+8, 2c+9; lane group g's D/8 columns
     uint32_t vw[4][D / 32];
-    bool nan_code = false;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int r = 2 * c + (t & 1) + (t >> 1) * 8;
@@ -357,68 +386,65 @@ __device__ void segment(const AttendParams& p, const Tile& x, int h, int u0, int
     }
     // Tokens that some rows of the tile see and others do not: a NaN code among
     // their values must not reach the latter as 0 * NaN.
-    const bool edge = !p.sel_width && u0 * kUnit + (s + 1) * kUnit > first_limit;
-    if (edge) {
+    if (!p.sel_width && (u0 + s + 1) * kUnit > first_limit) {
+      bool nan_code = false;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) nan_code = nan_code || nan_bytes(vw[t][k]) != 0;
-      if (__any_sync(kFullMask, nan_code)) poison<D>(sc, vw, acc);
+      if (__any_sync(kFullMask, nan_code)) poison<D, NT>(sc, vw, acc);
     }
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) {
-      const uint32_t lo01 = __byte_perm(vw[0][k], vw[1][k], 0x5140), hi01 = __byte_perm(vw[0][k], vw[1][k], 0x7362);
-      const uint32_t lo23 = __byte_perm(vw[2][k], vw[3][k], 0x5140), hi23 = __byte_perm(vw[2][k], vw[3][k], 0x7362);
-      mma16816(acc[4 * k], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(lo01)),
-               e4m3x2_to_f16x2(static_cast<uint16_t>(lo23)));
-      mma16816(acc[4 * k + 1], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(lo01 >> 16)),
-               e4m3x2_to_f16x2(static_cast<uint16_t>(lo23 >> 16)));
-      mma16816(acc[4 * k + 2], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(hi01)),
-               e4m3x2_to_f16x2(static_cast<uint16_t>(hi23)));
-      mma16816(acc[4 * k + 3], pf, e4m3x2_to_f16x2(static_cast<uint16_t>(hi01 >> 16)),
-               e4m3x2_to_f16x2(static_cast<uint16_t>(hi23 >> 16)));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t sel = half ? 0x7362 : 0x5140;
+        const uint32_t w01 = __byte_perm(vw[0][k], vw[1][k], sel), w23 = __byte_perm(vw[2][k], vw[3][k], sel);
+        const uint32_t a[4] = {cvt_lo(w01), cvt_hi(w01), cvt_lo(w23), cvt_hi(w23)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(acc[2 * k + half][nt], a, pf[nt][0], pf[nt][1]);
+      }
     }
-    __syncwarp();  // every lane has read the ring entry that the next copy overwrites
+    __syncwarp();  // every lane has read what the next copies and translations overwrite
   }
 
   // join the four warps
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    l[half] += __shfl_xor_sync(kFullMask, l[half], 1);
-    l[half] += __shfl_xor_sync(kFullMask, l[half], 2);
-  }
-#pragma unroll
-  for (int half = 0; half < 2; ++half)
-    if (isnan(l[half])) m[half] = 0.f;  // a row of NaN scores counts in the join
   cp_async_wait<0>();
   __syncthreads();
   float* jo = reinterpret_cast<float*>(smem);
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    float* row = jo + (warp * kStreamRows + g + 8 * half) * (D + 4);
-    // fragment column 2c+j of accumulator i is column (2c+j)*(D/8) + i
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int i = 0; i < D / 8; i += 4)
-        *reinterpret_cast<float4*>(row + (2 * c + j) * (D / 8) + i) =
-            make_float4(acc[i][half * 2 + j], acc[i + 1][half * 2 + j], acc[i + 2][half * 2 + j],
-                        acc[i + 3][half * 2 + j]);
-    if (c == 0) ml[warp * kStreamRows + g + 8 * half] = make_float2(m[half], l[half]);
-  }
+      for (int o = 4; o < 32; o <<= 1) l[nt][j] += __shfl_xor_sync(kFullMask, l[nt][j], o);
+      if (isnan(l[nt][j])) m[nt][j] = 0.f;  // a row of NaN scores counts in the join
+      const int i = 8 * nt + 2 * c + j;
+      float* row = jo + (warp * R + i) * (D + 4) + g * (D / 8);
+#pragma unroll
+      for (int k = 0; k < D / 16; k += 2)
+        *reinterpret_cast<float4*>(row + 2 * k) =
+            make_float4(acc[k][nt][j], acc[k][nt][2 + j], acc[k + 1][nt][j], acc[k + 1][nt][2 + j]);
+      if (g == 0) ml[warp * R + i] = make_float2(m[nt][j], l[nt][j]);
+    }
   __syncthreads();
-  store_rows<D, F16>(p, x, h, whole, part, jo, ml);
+  store_rows<D, NT, F16>(p, x, h, whole, part, jo, ml);
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kWarps * 32, 3) attend_stream_kernel(const __grid_constant__ AttendParams p) {
+template <int D, int NT>
+constexpr int kCtasPerSm = NT == 1 ? 4 : 3;
+
+template <int D, int NT, bool F16>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
+    attend_stream_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int R = 8 * NT;
   if (p.n_ctas == 0) {
     // one CTA per (tile, head); the last tiles of a causal sequence, which see most, first
     const int t = p.n_tiles - 1 - blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads;
-    const Tile x = tile_at<kStreamRows>(p, t);
+    const Tile x = tile_at<R>(p, t);
     if (x.rows <= 0) return;
-    segment<D, F16>(p, x, h, 0, tile_units<kUnit>(x), true, 0, smem);
+    segment<D, NT, F16>(p, x, h, 0, tile_units<kUnit>(x), true, 0, smem);
     return;
   }
   // Equal shares of all units, tile by tile and head by head.
@@ -427,7 +453,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_stream_kernel(const __g
   int total = 0;
   for (int t0 = 0; t0 < p.n_tiles; t0 += kWarps * 32) {
     const int t = t0 + threadIdx.x;
-    const int u = t < p.n_tiles ? tile_units<kUnit>(tile_at<kStreamRows>(p, t)) : 0;
+    const int u = t < p.n_tiles ? tile_units<kUnit>(tile_at<R>(p, t)) : 0;
     int all;
     const int before = block_scan_tiles<kWarps * 32>(u, &all, warp_sums);
     if (t < p.n_tiles) prefix[t] = total + before;
@@ -453,9 +479,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attend_stream_kernel(const __g
     const int64_t in = u - static_cast<int64_t>(prefix[lo]) * p.c.heads;
     const int h = static_cast<int>(in / tu), u0 = static_cast<int>(in % tu);
     const int u1 = static_cast<int>(min(static_cast<int64_t>(tu), u0 + (end - u)));
-    const Tile x = tile_at<kStreamRows>(p, lo);
-    segment<D, F16>(p, x, h, u0, u1, u0 == 0 && u1 == tu, 2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1),
-                    smem);
+    const Tile x = tile_at<R>(p, lo);
+    segment<D, NT, F16>(p, x, h, u0, u1, u0 == 0 && u1 == tu, 2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1),
+                        smem);
     first = false;
     u += u1 - u0;
   }
@@ -500,19 +526,20 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   }
 }
 
-template <int D, bool F16>
+template <int D, int NT, bool F16>
 cudaError_t go_stream(const AttendParams& p, int grid, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(attend_stream_kernel<D, F16>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  constexpr int kBytes = Smem<D, NT>::kBytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(attend_stream_kernel<D, NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  attend_stream_kernel<D, F16><<<grid, kWarps * 32, Smem<D>::kBytes, stream>>>(p);
+  attend_stream_kernel<D, NT, F16><<<grid, kWarps * 32, kBytes, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, int R, bool F16>
 cudaError_t go_join(const AttendParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles) * p.c.heads, R / 16);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles) * p.c.heads, R / 8);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -525,16 +552,28 @@ cudaError_t go_join(const AttendParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int attend_stream_ctas_per_sm(int D) { return 3; }
+int attend_stream_ctas_per_sm(int rows) { return rows <= 8 ? 4 : 3; }
 
-cudaError_t launch_attend_stream(const AttendParams& p, int D, bool f16, int grid, cudaStream_t stream) {
-  if (D == 128) return f16 ? go_stream<128, true>(p, grid, stream) : go_stream<128, false>(p, grid, stream);
-  return f16 ? go_stream<64, true>(p, grid, stream) : go_stream<64, false>(p, grid, stream);
+cudaError_t launch_attend_stream(const AttendParams& p, int D, int rows, bool f16, int grid, cudaStream_t stream) {
+#define HWR_GO(DD, NN) return f16 ? go_stream<DD, NN, true>(p, grid, stream) : go_stream<DD, NN, false>(p, grid, stream)
+  if (D == 128) {
+    if (rows == 8) HWR_GO(128, 1);
+    HWR_GO(128, 2);
+  }
+  if (rows == 8) HWR_GO(64, 1);
+  HWR_GO(64, 2);
+#undef HWR_GO
 }
 
-cudaError_t launch_attend_join(const AttendParams& p, int D, int R, bool f16, cudaStream_t stream) {
-  if (D == 128) return f16 ? go_join<128, 16, true>(p, stream) : go_join<128, 16, false>(p, stream);
-  return f16 ? go_join<64, 16, true>(p, stream) : go_join<64, 16, false>(p, stream);
+cudaError_t launch_attend_join(const AttendParams& p, int D, int rows, bool f16, cudaStream_t stream) {
+#define HWR_GO(DD, RR) return f16 ? go_join<DD, RR, true>(p, stream) : go_join<DD, RR, false>(p, stream)
+  if (D == 128) {
+    if (rows == 8) HWR_GO(128, 8);
+    HWR_GO(128, 16);
+  }
+  if (rows == 8) HWR_GO(64, 8);
+  HWR_GO(64, 16);
+#undef HWR_GO
 }
 
 }  // namespace hwr

@@ -105,13 +105,16 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   int sms = 0;
   st = device_status(&sms);
   if (st != INDEXER_OK) return st;
-  const int R = pl->rows = kStreamRows;
+  // rows that share a pass over the keys: of a query with a selection, of a
+  // sequence without
+  const int64_t most_rows = a->sel_width ? p.G : static_cast<int64_t>(a->max_q ? a->max_q : s->S) * p.G;
+  const int R = pl->rows = most_rows <= 8 ? 8 : 16;
   p.sel_tiles = (p.G + R - 1) / R;
   const int64_t tiles = a->sel_width ? s->S * p.sel_tiles : s->S * p.G / R + s->B;
   const int64_t items = tiles * c->heads;
   if (items > INT32_MAX - 1024) return INDEXER_EUNSUPPORTED;
   p.n_tiles = static_cast<int32_t>(tiles);
-  const int slots = sms * attend_stream_ctas_per_sm(c->D);
+  const int slots = sms * attend_stream_ctas_per_sm(R);
   // Fewer (tile, head)s than fill the SMs a few times over: the CTAs share all
   // keys equally, across tiles, and a second kernel joins the parts.
   const int64_t most_keys = a->sel_width ? a->sel_width : p.max_keys;
@@ -235,7 +238,7 @@ indexer_status indexer_cache_attend(const indexer_cache* cache, const indexer_se
   p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + pl.off_o);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (launch_attend_stream(p, pl.D, pl.f16, pl.grid, cs) != cudaSuccess) return INDEXER_ECUDA;
+  if (launch_attend_stream(p, pl.D, pl.rows, pl.f16, pl.grid, cs) != cudaSuccess) return INDEXER_ECUDA;
   if (p.n_ctas && launch_attend_join(p, pl.D, pl.rows, pl.f16, cs) != cudaSuccess) return INDEXER_ECUDA;
   return INDEXER_OK;
 }

@@ -90,11 +90,11 @@ __device__ __forceinline__ void rotate(const RotView& r, const uint4& raw, int s
   }
 }
 
-template <int D>
-__device__ __forceinline__ float row_max(float v) {
-#pragma unroll
-  for (int o = kLanes<D> / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
-  return v;
+// max that is NaN where either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 __device__ __forceinline__ uint2 pack_codes(const float (&y)[8]) {
@@ -137,21 +137,32 @@ __global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __r
       float y[8];
       rotate<D, F16>(rot, raw[u], sub, a, y);
       float m = 0.f;
-      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
+#pragma unroll
+      for (int o = kLanes<D> / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFullMask, m, o));
+      if (!ok || !(m < INFINITY)) m = NAN;  // the whole row becomes NaN codes
+      const float sc = m == 0.f ? 1.f : __fdiv_rn(m, 448.f), inv = __fdividef(1.f, sc);
+      // code = RNE_e4m3(y / sc).  y * inv is within 8 units in the last place of
+      // the quotient, which decides the code unless a border between two codes
+      // (a number of at most 5 significant bits: 19 zeros at the end) is that
+      // near; then the quotient itself is taken.
+      float z[8];
+      uint32_t gap = 0xFFFFFFFFu;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        m = fmaxf(m, fabsf(y[i]));
-        nan = nan || isnan(y[i]);
+        z[i] = y[i] * inv;
+        gap = min(gap, (__float_as_uint(z[i]) + 8u) & 0x7FFFFu);
       }
-      m = row_max<D>(nan ? INFINITY : m);
-      const float sc = !ok ? 1.f : m > 0.f ? __fdiv_rn(m, 448.f) : 1.f;
+      if (gap <= 16u) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = ok && m < INFINITY ? __fdiv_rn(y[i], sc) : NAN;
-      const uint2 code = pack_codes(y);
+        for (int i = 0; i < 8; ++i) z[i] = __fdiv_rn(y[i], sc);
+      }
+      const uint2 code = pack_codes(z);
       if (live && h + u < h1) {
         const int64_t o = t * H + h + u;
         *reinterpret_cast<uint2*>(codes + o * D + sub * 8) = code;
-        if (sub == 0) scale[o] = sc;
+        if (sub == 0) scale[o] = ok ? sc : 1.f;
       }
     }
   }
@@ -169,17 +180,20 @@ __device__ __forceinline__ float block_scale(float amax) {
 
 // Keys and values.  CTAs [0, kv_slots * kv_split): slot = one block of tokens
 // (floor(rows/block) + 2 slots a sequence), split over the 2*heads key and
-// value heads.  A (block, head) is taken by block/16 warps (one for blocks of
-// up to 16), 16 rows each, held in registers between the maximum and the
-// quantisation: every row is read once.  Then q: 8 warps x 256/D rows x a share
-// of the query heads per CTA.
+// value heads.  A (block, head) is taken by a team of warps, 4 warp steps of
+// rows each, whose 16-bit values stay in registers between the maximum and the
+// quantisation: every row is read once, and rotated twice.  Then q: 16 warps x
+// 256/D rows x a share of the query heads per CTA.
+constexpr int kAppendWarps = 16;
+constexpr int kSteps = 4;
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 1) cache_append_kernel(const __grid_constant__ AppendParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes<D>, rsub = lane / kLanes<D>;
   const int kv_ctas = p.kv_slots * p.kv_split;
   if (static_cast<int>(blockIdx.x) >= kv_ctas) {
     const int i = blockIdx.x - kv_ctas;
-    const int r = (i % p.q_slots * 8 + warp) * kRows<D> + rsub;
+    const int r = (i % p.q_slots * kAppendWarps + warp) * kRows<D> + rsub;
     const int h0 = i / p.q_slots * p.q_heads, h1 = min(p.Hq, h0 + p.q_heads);
     Angles a;
     bool ok = r < p.s.S && r < seq_row(p.s, p.s.B);
@@ -192,7 +206,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
     }
     const uint8_t* in = p.q + r * p.q_stride + sub * 16;
     uint8_t* out = p.q_out + (static_cast<int64_t>(r) * p.Hq) * (2 * D) + sub * 16;
-    constexpr int U = 4;
+    constexpr int U = 8;
     for (int h = h0; h < h1; h += U) {
       uint4 raw[U];
 #pragma unroll
@@ -233,45 +247,47 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
   const int hi_ok = bad_tail ? static_cast<int>(max(p.r.rows - t0, int64_t(lo))) : hi;
   if (hi_ok <= lo) return;
 
-  const int team = blk <= 16 ? 1 : blk >> 4;   // warps of a (block, head)
-  const int teams = 8 / team, in_team = warp % team;
+  constexpr int kTeamRows = kSteps * kRows<D>;  // rows of a warp
+  const int team = blk <= kTeamRows ? 1 : blk / kTeamRows;
+  const int teams = kAppendWarps / team, in_team = warp % team;
   const int jobs = 2 * p.c.heads, jobs_per = (jobs + p.kv_split - 1) / p.kv_split;
   const int j0 = part * jobs_per, j1 = min(jobs, j0 + jobs_per);
-  constexpr int STEPS = 16 / kRows<D>;  // warp steps of 16 rows
-  __shared__ float part_max[8];
+  __shared__ float part_max[kAppendWarps];
   const int64_t sc0 = (page * p.c.page_blocks + (off >> p.c.block_shift)) * p.c.heads;
   const int64_t tok0 = page * p.c.page16 + off * p.c.token16;
+  const int tw = in_team * kTeamRows + rsub;  // the lane's row of warp step i: tw + i * kRows
   for (int jb = j0; jb < j1; jb += teams) {
     const int job = jb + warp / team;
     const bool on = job < j1;
     const bool is_v = on && job >= p.c.heads;
     const int h = on ? (is_v ? job - p.c.heads : job) : 0;
-    const uint8_t* src = (is_v ? p.v : p.k) + h * (2 * D) + sub * 16;
-    uint4 raw[STEPS];
+    const uint8_t* src = (is_v ? p.v : p.k) + h * (2 * D) + sub * 16 + (row0 + (t0 - past) + tw) * p.kv_stride;
+    uint4 raw[kSteps];
+    uint32_t in = 0;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int t = in_team * 16 + i * kRows<D> + rsub;
+    for (int i = 0; i < kSteps; ++i) {
+      const int t = tw + i * kRows<D>;
       raw[i] = make_uint4(0, 0, 0, 0);
-      if (on && t >= lo && t < hi_ok)
-        raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + (row0 + (t0 - past) + t) * p.kv_stride));
+      if (on && t >= lo && t < hi_ok) {
+        raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + i * kRows<D> * p.kv_stride));
+        in |= 1u << i;
+      }
     }
-    float y[STEPS][8];
+    float* sp = (is_v ? p.c.vs : p.c.ks) + sc0 + h;
+    const float old = on && lo > 0 ? *sp : 0.f;
+    RotView r = p.r;
+    if (is_v) r.rot = 0;
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int t = in_team * 16 + i * kRows<D> + rsub;
-      const bool in = on && t >= lo && t < hi_ok;
-      RotView r = p.r;
-      if (is_v) r.rot = 0;
+    for (int i = 0; i < kSteps; ++i) {
       Angles a;
-      if (in && r.rot) load_angles(r, t0 + t, sub, a);
-      rotate<D, F16>(r, raw[i], sub, a, y[i]);
+      float y[8];
+      if ((in >> i & 1) && r.rot) load_angles(r, t0 + tw + i * kRows<D>, sub, a);
+      rotate<D, F16>(r, raw[i], sub, a, y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float v = fabsf(y[i][e]);
-        const bool fin = v < INFINITY;
-        if (in && fin) m = fmaxf(m, v);
-        if (!fin) y[i][e] = NAN;
+        const float v = fabsf(y[e]);
+        if ((in >> i & 1) && v < INFINITY) m = fmaxf(m, v);
       }
     }
 #pragma unroll
@@ -281,33 +297,32 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const __grid_constant
       __syncthreads();
       for (int w = 0; w < team; ++w) m = fmaxf(m, part_max[warp - in_team + w]);
     }
-    float* sp = (is_v ? p.c.vs : p.c.ks) + sc0 + h;
     const float need = block_scale(m);
-    const float old = on && lo > 0 ? *sp : 0.f;
     const float sc = lo > 0 ? fmaxf(need, fmaxf(old, kMinBlockScale)) : need;
     // the old scale and the maxima are read before they are overwritten
     if (team > 1)
       __syncthreads();
     else
       __syncwarp();
-    uint8_t* dst = (is_v ? p.c.v : p.c.k) + (tok0 + h * p.c.head16) * 16 + sub * 8;
+    uint8_t* dst = (is_v ? p.c.v : p.c.k) + (tok0 + h * p.c.head16 + tw * p.c.token16) * 16 + sub * 8;
     const float inv = 1.f / sc;  // a power of two: exact
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int t = in_team * 16 + i * kRows<D> + rsub;
-      if (!on || t >= blk) continue;
-      uint2* at = reinterpret_cast<uint2*>(dst + t * p.c.token16 * 16);
-      if (t >= lo && t < hi_ok) {
-        float z[8];
+    for (int i = 0; i < kSteps; ++i) {
+      const int t = tw + i * kRows<D>;
+      uint2* at = reinterpret_cast<uint2*>(dst + i * kRows<D> * p.c.token16 * 16);
+      Angles a;
+      float z[8];
+      if ((in >> i & 1) && r.rot) load_angles(r, t0 + t, sub, a);
+      rotate<D, F16>(r, raw[i], sub, a, z);
+      if (in >> i & 1) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = y[i][e] * inv;
+        for (int e = 0; e < 8; ++e) z[e] = fabsf(z[e]) < INFINITY ? z[e] * inv : NAN;
         *at = pack_codes(z);
-      } else if (t < lo && sc != old) {
+      } else if (on && t < lo && sc != old) {
         // an earlier token of a block whose scale rises
         const float f = old * inv;
         const uint2 was = *at;
         const uint32_t ww[2] = {was.x, was.y};
-        float z[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t hh = e4m3x2_to_f16x2(static_cast<uint16_t>(ww[e >> 1] >> (16 * (e & 1))));
@@ -349,13 +364,15 @@ cudaError_t launch_rotate_quantise(const void* x, int64_t S, int H, int D, bool 
 cudaError_t launch_cache_append(AppendParams p, int D, bool f16, int sms, cudaStream_t stream) {
   if (p.s.S == 0 || p.s.B == 0) return cudaSuccess;
   p.kv_slots = static_cast<int32_t>(p.s.S / p.c.block + 2 * static_cast<int64_t>(p.s.B));
-  const int team = p.c.block <= 16 ? 1 : p.c.block / 16, teams = 8 / team;
+  const int team_rows = kSteps * (256 / D), team = p.c.block <= team_rows ? 1 : p.c.block / team_rows;
+  const int teams = kAppendWarps / team;
   p.kv_split = 1;
   while (static_cast<int64_t>(p.kv_slots) * p.kv_split < 2 * sms && p.kv_split * teams < 2 * p.c.heads) p.kv_split *= 2;
   p.q_slots = p.q_heads = 0;
   int64_t q_ctas = 0;
   if (p.q) {
-    p.q_slots = static_cast<int32_t>((p.s.S + 8 * (256 / D) - 1) / (8 * (256 / D)));
+    const int cta_rows = kAppendWarps * (256 / D);
+    p.q_slots = static_cast<int32_t>((p.s.S + cta_rows - 1) / cta_rows);
     int split = 1;
     while (static_cast<int64_t>(p.q_slots) * split < 2 * sms && split * 4 <= p.Hq) split *= 2;
     p.q_heads = (p.Hq + split - 1) / split;
@@ -363,7 +380,7 @@ cudaError_t launch_cache_append(AppendParams p, int D, bool f16, int sms, cudaSt
   }
   const int64_t grid = static_cast<int64_t>(p.kv_slots) * p.kv_split + q_ctas;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-#define HWR_GO(DD, FF) cache_append_kernel<DD, FF><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p)
+#define HWR_GO(DD, FF) cache_append_kernel<DD, FF><<<static_cast<unsigned>(grid), kAppendWarps * 32, 0, stream>>>(p)
   if (D == 128) {
     if (f16) HWR_GO(128, true); else HWR_GO(128, false);
   } else {

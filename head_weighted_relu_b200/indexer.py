@@ -426,7 +426,11 @@ def pool_keys(k, pool_coef, ratio, stream=None):
 # ---------------------------------------------------------------------------
 
 _ACT = {torch.bfloat16: ACT_BF16, torch.float16: ACT_FP16}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 
+
+# The checks run on every call of a decode step, so they read each attribute of a
+# tensor once and build a message only where they fail.
 
 def _act(x, what):
     a = _ACT.get(x.dtype)
@@ -435,57 +439,69 @@ def _act(x, what):
     return a
 
 
-def _need(ok, message):
-    if not ok:
-        raise ValueError(message)
-
-
-def _tokens(x, what, device, shape=None, dtype=None):
-    """Token stride of activations [S, H, D] whose heads are packed (so a slice of
-    a wider projection passes unchanged)."""
-    _need(x.dim() == 3 and x.device == device and (dtype is None or x.dtype == dtype)
-          and (shape is None or tuple(x.shape) == tuple(shape)),
-          f"{what}: expected {'[S, H, D]' if shape is None else tuple(shape)}"
-          f"{'' if dtype is None else f' {dtype}'} on {device}, got {tuple(x.shape)} {x.dtype} on {x.device}")
-    S, H, D = x.shape
-    _need(x.numel() == 0 or ((D == 1 or x.stride(2) == 1) and (H == 1 or x.stride(1) == D)),
-          f"{what}: heads must be packed within a token (strides {x.stride()})")
-    return x.stride(0) if S > 1 else H * D
+def _tokens(x, what, device, shape, dtype):
+    """Token stride of activations `shape` = (S, H, D) whose heads are packed (so a
+    slice of a wider projection passes unchanged)."""
+    if x.shape != shape or x.dtype != dtype or x.get_device() != device:
+        raise ValueError(f"{what}: expected {tuple(shape)} {dtype} on cuda:{device}, "
+                         f"got {tuple(x.shape)} {x.dtype} on {x.device}")
+    S, H, D = shape
+    st, sh, sd = x.stride()
+    if (sd != 1 or (sh != D and H > 1)) and x.numel():
+        raise ValueError(f"{what}: heads must be packed within a token (strides {x.stride()})")
+    return st if S > 1 else H * D
 
 
 def _ints(x, what, device, shape):
-    _need(x.dtype == torch.int32 and x.device == device and tuple(x.shape) == tuple(shape) and x.is_contiguous(),
-          f"{what} must be a contiguous {tuple(shape)} int32 tensor on {device}")
+    if x.dtype != torch.int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous {tuple(shape)} int32 tensor on cuda:{device}")
     return x.data_ptr()
+
+
+def _result(x, what, device, shape, dtype):
+    if x.dtype != dtype or x.shape != shape or not x.is_contiguous() or x.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous {tuple(shape)} {dtype} tensor on cuda:{device}")
+    return x
+
+
+_NO_ROTATION = Rotation(None, 0, 0, 0)
 
 
 def _rotation(table, interleaved, device):
     if table is None:
-        return Rotation(None, 0, 0, 0)
-    _need(table.dim() == 2 and table.dtype == torch.float32 and table.is_contiguous() and table.device == device,
-          f"the rotation table must be a contiguous [positions, rot_dim] float32 tensor on {device}")
-    return Rotation(table.data_ptr(), table.shape[0], table.shape[1], 1 if interleaved else 0)
+        return _NO_ROTATION
+    if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous() or table.get_device() != device:
+        raise ValueError(f"the rotation table must be a contiguous [positions, rot_dim] float32 tensor on cuda:{device}")
+    rows, rot_dim = table.shape
+    return Rotation(table.data_ptr(), rows, rot_dim, 1 if interleaved else 0)
 
 
-class _On:
-    """Makes `device` current for the library call and names the stream: the
-    caller's, or the device's current one."""
+def _device_of(x):
+    i = x.get_device()
+    if i < 0:
+        raise ValueError(f"tensors must be on a CUDA device, not {x.device}")
+    return i
 
-    def __init__(self, device, stream):
-        _need(device.type == "cuda", f"tensors must be on a CUDA device, not {device}")
-        self.device, self.stream = device, stream
 
-    def __enter__(self):
-        self.guard = None
-        if torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return s.cuda_stream
+def _call(fn, device, stream, *args):
+    """lib.fn(*args, stream) with `device` current, on the caller's stream or the
+    device's current one."""
+    if torch.cuda.current_device() == device:
+        status = getattr(_lib, fn)(*args, (stream or torch.cuda.current_stream(device)).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = getattr(_lib, fn)(*args, (stream or torch.cuda.current_stream(device)).cuda_stream)
+    if status != 0:
+        raise IndexerError(fn, status)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _new(stream, device, shape, dtype):
+    """An uninitialised tensor for the call: on the call's stream, so that its
+    memory is not handed to other work while the call may still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -503,25 +519,29 @@ def rotate_quantise(x, positions=None, table=None, interleaved=False, out=None, 
 
     positions [S] int32 (None: 0, 1, ...), table as from `rope_table` (None: no
     rotation).  out = (codes, scale) writes into given contiguous tensors, e.g.
-    the next rows of the indexer's key arrays.
+    the next rows of the indexer's key arrays.  status: a [1] int32 tensor that
+    bits are ORed into.
     """
+    device = _device_of(x)
     act = _act(x, "x")
-    stride = _tokens(x, "x", x.device)
-    S, H, D = x.shape
-    rot = _rotation(table, interleaved, x.device)
-    pos = None if positions is None else _ints(positions, "positions", x.device, (S,))
-    with _On(x.device, stream) as cs:
-        if out is None:
-            out = (torch.empty((S, H, D), dtype=torch.uint8, device=x.device),
-                   torch.empty((S, H), dtype=torch.float32, device=x.device))
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x must be [S, H, D], not {tuple(shape)}")
+    S, H, D = shape
+    stride = _tokens(x, "x", device, shape, x.dtype)
+    rot = _rotation(table, interleaved, device)
+    pos = None if positions is None else _ints(positions, "positions", device, (S,))
+    if out is None:
+        codes = _new(stream, device, shape, torch.uint8)
+        scale = _new(stream, device, (S, H), torch.float32)
+    else:
         codes, scale = out
-        _need(codes.dtype in (torch.uint8, torch.float8_e4m3fn) and codes.is_contiguous() and codes.numel() == S * H * D
-              and codes.device == x.device and scale.dtype == torch.float32 and scale.is_contiguous()
-              and scale.numel() == S * H and scale.device == x.device,
-              "out must be contiguous codes (S*H*D uint8) and scales (S*H float32) on x's device")
-        _check("indexer_rotate_quantise", _lib.indexer_rotate_quantise(
-            x.data_ptr(), S, H, D, act, stride, pos, rot, codes.data_ptr(), scale.data_ptr(),
-            None if status is None else _ints(status, "status", x.device, (1,)), cs))
+        if not (codes.dtype in _CODES and codes.is_contiguous() and codes.numel() == S * H * D
+                and codes.get_device() == device and scale.dtype == torch.float32 and scale.is_contiguous()
+                and scale.numel() == S * H and scale.get_device() == device):
+            raise ValueError("out must be contiguous codes (S*H*D of them) and float32 scales (S*H) on x's device")
+    _call("indexer_rotate_quantise", device, stream, x.data_ptr(), S, H, D, act, stride, pos, rot, codes.data_ptr(),
+          scale.data_ptr(), None if status is None else _ints(status, "status", device, (1,)))
     return codes, scale
 
 
@@ -537,38 +557,42 @@ class KVCache(NamedTuple):
 
     def descriptor(self) -> CacheDesc:
         k, v, ks, vs = self
-        _need(k.dim() == 4 and v.shape == k.shape and v.stride() == k.stride() and k.stride(3) == 1
-              and k.dtype in (torch.uint8, torch.float8_e4m3fn) and v.dtype == k.dtype and v.device == k.device,
-              "k and v must be alike: [pages, page_size, heads, D] e4m3 codes, the last dimension contiguous")
-        pages, page_size, heads, D = k.shape
-        _need(ks.dim() == 3 and ks.shape == vs.shape and ks.shape[0] == pages and ks.shape[2] == heads
-              and 0 < ks.shape[1] <= page_size and page_size % ks.shape[1] == 0
-              and ks.dtype == vs.dtype == torch.float32 and ks.is_contiguous() and vs.is_contiguous()
-              and ks.device == vs.device == k.device,
-              "k_scale and v_scale must be contiguous [pages, page_size // block, heads] float32 tensors")
-        sp, st, sh, _ = k.stride()
-        return CacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, sp, st, sh,
-                         page_size, page_size // ks.shape[1], heads, D)
+        shape, strides = k.shape, k.stride()
+        if (len(shape) != 4 or v.shape != shape or v.stride() != strides or strides[3] != 1 or k.dtype not in _CODES
+                or v.dtype not in _CODES or v.get_device() != k.get_device()):
+            raise ValueError("k and v must be alike: [pages, page_size, heads, D] e4m3 codes, the last dimension "
+                             "contiguous")
+        pages, page_size, heads, D = shape
+        sshape = ks.shape
+        blocks = sshape[1] if len(sshape) == 3 else 0
+        if (sshape != (pages, blocks, heads) or vs.shape != sshape or not 0 < blocks <= page_size
+                or page_size % blocks or ks.dtype != torch.float32 or vs.dtype != torch.float32
+                or not (ks.is_contiguous() and vs.is_contiguous())
+                or not ks.get_device() == vs.get_device() == k.get_device()):
+            raise ValueError("k_scale and v_scale must be contiguous [pages, page_size // block, heads] float32 tensors "
+                             "on the device of k")
+        return CacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, strides[0], strides[1],
+                         strides[2], page_size, page_size // blocks, heads, D)
 
 
 def allocate_cache(pages, page_size, heads, D, block=16, device="cuda") -> KVCache:
     """A cache for pages * page_size tokens, uninitialised (what a sequence has
     not been given by `cache_append` is never read)."""
-    _need(block >= 1 and page_size % block == 0, "page_size must be a multiple of block")
+    if block < 1 or page_size % block:
+        raise ValueError("page_size must be a multiple of block")
     k, v = (torch.empty((pages, page_size, heads, D), dtype=torch.uint8, device=device) for _ in range(2))
     ks, vs = (torch.empty((pages, page_size // block, heads), dtype=torch.float32, device=device) for _ in range(2))
     return KVCache(k, v, ks, vs)
 
 
 def _sequences(S, cu_q, kv_len, page_table, device) -> Sequences:
-    B = kv_len.shape[0] if kv_len.dim() == 1 else -1
-    _need(page_table.dim() == 2 and page_table.shape[0] == B and page_table.dtype == torch.int32
-          and page_table.device == device and (page_table.numel() == 0 or page_table.stride(1) == 1
-                                               or page_table.shape[1] == 1),
-          f"page_table must be a [{B}, pages] int32 tensor on {device} with contiguous rows")
+    B = kv_len.numel()
+    shape = page_table.shape
+    if (len(shape) != 2 or shape[0] != B or page_table.dtype != torch.int32 or page_table.get_device() != device
+            or (page_table.stride(1) != 1 and shape[1] > 1)):
+        raise ValueError(f"page_table must be a [{B}, pages] int32 tensor on cuda:{device} with contiguous rows")
     return Sequences(S, _ints(cu_q, "cu_q", device, (B + 1,)), _ints(kv_len, "kv_len", device, (B,)),
-                     page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]) if B > 1 else
-                     page_table.shape[1], page_table.shape[1], B)
+                     page_table.data_ptr(), page_table.stride(0) if B > 1 else shape[1], shape[1], B)
 
 
 def cache_append(cache: KVCache, k, v, cu_q, kv_len, page_table, table=None, interleaved=False, q=None, q_out=None,
@@ -583,29 +607,31 @@ def cache_append(cache: KVCache, k, v, cu_q, kv_len, page_table, table=None, int
     rows are returned (in q_out, if given); rows that belong to no sequence are
     left as they were.  status: a [1] int32 tensor that bits are ORed into.
     """
-    device = cache.k.device
+    device = _device_of(cache.k)
     desc = cache.descriptor()
-    S = k.shape[0]
+    S, dtype = k.shape[0], k.dtype
     act = _act(k, "k")
-    stride = _tokens(k, "k", device, (S, desc.heads, desc.D))
-    _need(_tokens(v, "v", device, (S, desc.heads, desc.D), k.dtype) == stride, "k and v must have the same strides")
+    shape = (S, desc.heads, desc.D)
+    stride = _tokens(k, "k", device, shape, dtype)
+    if _tokens(v, "v", device, shape, dtype) != stride:
+        raise ValueError("k and v must have the same strides")
     seqs = _sequences(S, cu_q, kv_len, page_table, device)
     rot = _rotation(table, interleaved, device)
     q_heads = q_stride = 0
-    with _On(device, stream) as cs:
-        if q is not None:
-            q_heads = q.shape[1]
-            q_stride = _tokens(q, "q", device, (S, q_heads, desc.D), k.dtype)
-            if q_out is None:
-                q_out = torch.empty((S, q_heads, desc.D), dtype=q.dtype, device=device)
-            _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.device == device
-                  and q_out.is_contiguous(), "q_out must be contiguous and like q")
+    qp = qo = None
+    if q is not None:
+        shape = q.shape
+        q_heads = shape[1] if len(shape) == 3 else 0
+        q_stride = _tokens(q, "q", device, (S, q_heads, desc.D), dtype)
+        if q_out is None:
+            q_out = _new(stream, device, shape, dtype)
         else:
-            _need(q_out is None, "q_out without q")
-        _check("indexer_cache_append", _lib.indexer_cache_append(
-            desc, seqs, k.data_ptr(), v.data_ptr(), stride, act, rot, None if q is None else q.data_ptr(), q_heads,
-            q_stride, None if q_out is None else q_out.data_ptr(),
-            None if status is None else _ints(status, "status", device, (1,)), cs))
+            _result(q_out, "q_out", device, shape, dtype)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _call("indexer_cache_append", device, stream, desc, seqs, k.data_ptr(), v.data_ptr(), stride, act, rot, qp, q_heads,
+          q_stride, qo, None if status is None else _ints(status, "status", device, (1,)))
     return q_out
 
 
@@ -619,49 +645,58 @@ def cache_attend(cache: KVCache, q, cu_q, kv_len, page_table, scale=None, causal
     causal=False all of them; selected = (idx [S, W], len [S]) int32, as `topk`
     returns them for positions counted from the sequence's start, narrows that to
     the positions named.  A row that sees nothing gives 0 and -inf.  scale
-    defaults to D ** -0.5.  max_q: rows of the longest sequence, if known (a
-    speed hint).  workspace: a uint8 tensor kept by the caller (its size from
-    `cache_attend_workspace_bytes`); by default it is allocated for the call.
+    defaults to D ** -0.5.  max_q: rows of the longest sequence, if known (it
+    chooses the kernel: results may differ by roundings).  workspace: a uint8
+    tensor kept by the caller (its size from `cache_attend_workspace_bytes`); by
+    default it is allocated for the call.
     """
-    device = cache.k.device
+    device = _device_of(cache.k)
     desc = cache.descriptor()
-    act = _act(q, "q")
-    S, Hq = q.shape[0], q.shape[1] if q.dim() == 3 else -1
-    stride = _tokens(q, "q", device, (S, Hq, desc.D))
+    act, dtype = _act(q, "q"), q.dtype
+    shape = q.shape
+    S, Hq = shape[0], shape[1] if len(shape) == 3 else 0
+    stride = _tokens(q, "q", device, (S, Hq, desc.D), dtype)
     seqs = _sequences(S, cu_q, kv_len, page_table, device)
     si = sl = None
     width = 0
     if selected is not None:
         idx, lens = selected
-        _need(idx.dim() == 2 and idx.shape[1] > 0, "selected indices must be [S, W] with W > 0")
-        width = idx.shape[1]
+        width = idx.shape[-1]
+        if width < 1:
+            raise ValueError("selected indices must be [S, W] with W > 0")
         si, sl = _ints(idx, "selected indices", device, (S, width)), _ints(lens, "selected lengths", device, (S,))
     att = Attention(Hq, act, 1 if causal else 0, width, max_q, scale if scale is not None else 1 / math.sqrt(desc.D))
-    with _On(device, stream) as cs:
-        n = ctypes.c_size_t()
-        _check("indexer_cache_attend_workspace_bytes",
-               _lib.indexer_cache_attend_workspace_bytes(desc, seqs, att, n))
-        if workspace is None:
-            workspace = torch.empty((n.value,), dtype=torch.uint8, device=device)
-        _need(workspace.device == device and workspace.is_contiguous(), f"workspace must be contiguous on {device}")
-        if out is None:
-            out = torch.empty((S, Hq, desc.D), dtype=q.dtype, device=device)
-        _need(out.shape == q.shape and out.dtype == q.dtype and out.device == device and out.is_contiguous(),
-              "out must be contiguous and like q")
-        lse = torch.empty((S, Hq), dtype=torch.float32, device=device) if with_lse else None
-        _check("indexer_cache_attend", _lib.indexer_cache_attend(
-            desc, seqs, att, q.data_ptr(), stride, si, sl, out.data_ptr(), None if lse is None else lse.data_ptr(),
-            None if status is None else _ints(status, "status", device, (1,)), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), cs))
+    if workspace is None:
+        workspace = _new(stream, device, (_attend_workspace(device, desc, seqs, att),), torch.uint8)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{device}")
+    if out is None:
+        out = _new(stream, device, shape, dtype)
+    else:
+        _result(out, "out", device, shape, dtype)
+    lse = _new(stream, device, (S, Hq), torch.float32) if with_lse else None
+    _call("indexer_cache_attend", device, stream, desc, seqs, att, q.data_ptr(), stride, si, sl, out.data_ptr(),
+          None if lse is None else lse.data_ptr(),
+          None if status is None else _ints(status, "status", device, (1,)), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return (out, lse) if with_lse else out
 
 
-def cache_attend_workspace_bytes(cache: KVCache, q, cu_q, kv_len, page_table, selected_width=0) -> int:
-    """Bytes of workspace for `cache_attend` on these tensors' shapes."""
-    desc = cache.descriptor()
-    seqs = _sequences(q.shape[0], cu_q, kv_len, page_table, cache.k.device)
+def _attend_workspace(device, desc, seqs, att) -> int:
     n = ctypes.c_size_t()
-    with _On(cache.k.device, None):
-        _check("indexer_cache_attend_workspace_bytes", _lib.indexer_cache_attend_workspace_bytes(
-            desc, seqs, Attention(q.shape[1], _act(q, "q"), 1, selected_width, 0, 1.0), n))
+    if torch.cuda.current_device() == device:
+        status = _lib.indexer_cache_attend_workspace_bytes(desc, seqs, att, n)
+    else:
+        with torch.cuda.device(device):
+            status = _lib.indexer_cache_attend_workspace_bytes(desc, seqs, att, n)
+    if status != 0:
+        raise IndexerError("indexer_cache_attend_workspace_bytes", status)
     return n.value
+
+
+def cache_attend_workspace_bytes(cache: KVCache, q, cu_q, kv_len, page_table, selected_width=0, max_q=0) -> int:
+    """Bytes of workspace for `cache_attend` on these tensors' shapes."""
+    device = _device_of(cache.k)
+    desc = cache.descriptor()
+    return _attend_workspace(device, desc, _sequences(q.shape[0], cu_q, kv_len, page_table, device),
+                             Attention(q.shape[1], _act(q, "q"), 1, selected_width, max_q, 1.0))

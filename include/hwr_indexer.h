@@ -479,7 +479,8 @@ typedef struct {
   int32_t act;        /* indexer_act of q and out */
   int32_t causal;     /* 0 or 1 */
   int32_t sel_width;  /* 0: no selection */
-  int32_t max_q;      /* rows of the longest sequence, or 0 if unknown (a speed hint only) */
+  int32_t max_q;      /* rows of the longest sequence, or 0 if unknown: it
+                         chooses the kernel, and so may change roundings */
   float scale;        /* finite */
 } indexer_attention;
 
