@@ -116,12 +116,11 @@ __device__ __forceinline__ int64_t share_owner(int64_t unit, int64_t u, int64_t 
 
 // The token that key entry `e` of a tile stands for, as the kernels read it.
 struct TokenEntry {
-  uint32_t off16;  // offset of the token in the cache, in units of 16 bytes, without the head
+  uint32_t off16;  // offset of the token in the cache, in units of 16 bytes, without the head (0 for none)
   int32_t pos;     // its position; INT_MAX where nothing is to be seen
   float ks;        // key scale
   float lvs;       // log2 of the value scale
 };
-constexpr uint32_t kNoToken = 0xFFFFFFFFu;
 
 // Translation of a key entry of (tile, head) to its token in three dependent
 // loads, so that a caller can issue each well before its value is used.  An
@@ -141,7 +140,7 @@ struct Translate {
       : p(p_), x(x_), h(h_), end(end_) {
     sel = p.sel_width ? p.sel_idx + static_cast<int64_t>(x.row) * p.sel_width : nullptr;
     pages = p.s.pages + x.b * p.s.page_stride;
-    seen = p.sel_width ? min(min(x.len, row_limit(p, x, x.first)), INT32_MAX) : 0;
+    seen = p.sel_width ? min(x.len, row_limit(p, x, x.first)) : 0;
   }
   __device__ __forceinline__ Index index(int e) const {
     if (e >= end || e < 0) return Index{INT32_MAX};
@@ -157,7 +156,7 @@ struct Translate {
     return r;
   }
   __device__ __forceinline__ Scale scale(const Page& g) const {
-    Scale r{INT32_MAX, kNoToken, 0.f, 1.f};
+    Scale r{INT32_MAX, 0, 0.f, 1.f};
     if (g.pos == INT32_MAX) return r;
     if (g.page < 0 || g.page >= p.c.n_pages) {
       if (p.status) atomicOr(p.status, kStatusToken);

@@ -131,21 +131,22 @@ __device__ __forceinline__ void load_q(const AttendParams& p, const Tile& x, int
   }
 }
 
+// Copies one step: 16 rows of D/16 chunks, of K and of V.  kbase, vbase: the
+// lane's chunk of token 0.
 template <int D>
-__device__ __forceinline__ void issue_step(const AttendParams& p, const TokenEntry* table, int64_t head,
+__device__ __forceinline__ void issue_step(const TokenEntry* table, const uint8_t* kbase, const uint8_t* vbase,
                                            uint32_t ring) {
-  // 16 rows of D/16 chunks, of K and of V
   const int lane = threadIdx.x & 31;
   constexpr int kCh = D / 16, kPer = kCh * kStep / 32;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int r = (i * 32 + lane) / kCh, ch = lane % kCh;
-    const uint32_t off = table[r].off16;
-    const bool on = off != kNoToken;
-    const int64_t at = on ? (static_cast<int64_t>(off) + head + ch) * 16 : 0;
-    const uint32_t dst = ring + chunk_at<D>(r, ch);
-    cp_async16(dst, p.c.k + at, on);
-    cp_async16(dst + kStep * D, p.c.v + at, on);
+    const int r = i * (32 / kCh) + lane / kCh;
+    const uint2 e = *reinterpret_cast<const uint2*>(table + r);
+    const bool on = e.y != INT32_MAX;
+    const int64_t at = static_cast<int64_t>(e.x) << 4;
+    const uint32_t dst = ring + chunk_at<D>(r, lane % kCh);
+    cp_async16(dst, kbase + at, on);
+    cp_async16(dst + kStep * D, vbase + at, on);
   }
   cp_async_commit();
 }
@@ -245,7 +246,9 @@ __device__ void segment(const AttendParams& p, const Tile& x, int h, int u0, int
   TokenEntry* table = reinterpret_cast<TokenEntry*>(smem + L::kData) + warp * (kTableSteps * kStep);
   float2* ml = reinterpret_cast<float2*>(smem + L::kData + L::kTable);
   const uint32_t ring = smem_u32(smem) + warp * (kDepth * L::kStepBytes);
-  const int64_t head = h * p.c.head16;
+  const int64_t chunk = (h * p.c.head16 + lane % (D / 16)) * 16;
+  const uint8_t* kbase = p.c.k + chunk;
+  const uint8_t* vbase = p.c.v + chunk;
   const int n = u1 - u0;  // steps of this warp
 
   __syncthreads();  // the previous segment's buffers are free
@@ -281,7 +284,7 @@ __device__ void segment(const AttendParams& p, const Tile& x, int h, int u0, int
 #pragma unroll
   for (int i = 0; i < kDepth - 1; ++i) {
     if (i < n)
-      issue_step<D>(p, table + i * kStep, head, ring + i * L::kStepBytes);
+      issue_step<D>(table + i * kStep, kbase, vbase, ring + i * L::kStepBytes);
     else
       cp_async_commit();
   }
@@ -300,7 +303,7 @@ __device__ void segment(const AttendParams& p, const Tile& x, int h, int u0, int
     }
     const int next = slot >= 1 ? slot - 1 : kDepth - 1;  // the entry of step s - 1, free now: (s + 2) % 3
     if (s + 2 < n)
-      issue_step<D>(p, table + ((s + 2) & 3) * kStep, head, ring + next * L::kStepBytes);
+      issue_step<D>(table + ((s + 2) & 3) * kStep, kbase, vbase, ring + next * L::kStepBytes);
     else
       cp_async_commit();
     cp_async_wait<kDepth - 1>();
