@@ -60,8 +60,7 @@ struct Tile {
   int row;       // the query's activation row (selection)
 };
 
-template <int R>
-__device__ __forceinline__ Tile tile_at(const AttendParams& p, int t) {
+__device__ __forceinline__ Tile tile_at(const AttendParams& p, int t, int R) {
   Tile x;
   x.rows = 0;
   x.n_keys = 0;
@@ -108,10 +107,38 @@ __device__ __forceinline__ int row_limit(const AttendParams& p, const Tile& x, i
   return p.causal ? x.len - x.n_q + pair / p.G + 1 : x.len;
 }
 
+// prefix[t]: the units of the tiles before t, for one head; prefix[n_tiles]: of
+// all, which is returned.  For CTAs of THREADS threads that share a launch's
+// units; all take part.  CTA 0 leaves a copy in the workspace for the join.
+template <int UNIT, int THREADS>
+__device__ __forceinline__ int tile_prefix(const AttendParams& p, int R, int* prefix, int* warp_sums);
+
 // CTA c of n <= u takes units [start(c), start(c+1)) of u: one or more each.
 __host__ __device__ __forceinline__ int64_t share_start(int64_t c, int64_t u, int64_t n) { return c * u / n; }
 __device__ __forceinline__ int64_t share_owner(int64_t unit, int64_t u, int64_t n) {
   return ((unit + 1) * n - 1) / u;
+}
+
+// The piece of a CTA's share that starts at unit u: units [u0, u1) of (tile, h).
+struct Piece {
+  int tile, h, u0, u1;
+  bool whole;  // all of the (tile, head)'s units
+};
+__device__ __forceinline__ Piece piece_at(const AttendParams& p, const int* prefix, int64_t u, int64_t end) {
+  int lo = 0, hi = p.n_tiles - 1;  // the last tile that starts at or before u (empty ones start with the next)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(prefix[mid]) * p.c.heads <= u) lo = mid; else hi = mid - 1;
+  }
+  const int tu = prefix[lo + 1] - prefix[lo];
+  const int64_t in = u - static_cast<int64_t>(prefix[lo]) * p.c.heads;
+  Piece r;
+  r.tile = lo;
+  r.h = static_cast<int>(in / tu);
+  r.u0 = static_cast<int>(in % tu);
+  r.u1 = static_cast<int>(min(static_cast<int64_t>(tu), r.u0 + (end - u)));
+  r.whole = r.u0 == 0 && r.u1 == tu;
+  return r;
 }
 
 // The token that key entry `e` of a tile stands for, as the kernels read it.
@@ -199,35 +226,48 @@ __device__ __forceinline__ float row_pow2(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-template <int N>
-__device__ __forceinline__ int block_scan_tiles(int v, int* total, int* warp_sums) {
-  // exclusive prefix over N threads
+template <int UNIT, int THREADS>
+__device__ __forceinline__ int tile_prefix(const AttendParams& p, int R, int* prefix, int* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  int total = 0;
+  for (int t0 = 0; t0 < p.n_tiles; t0 += THREADS) {
+    const int t = t0 + threadIdx.x;
+    const int v = t < p.n_tiles ? tile_units<UNIT>(tile_at(p, t, R)) : 0;
+    int inc = v;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFullMask, inc, o);
-    if (lane >= o) inc += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = inc;
-  __syncthreads();
-  int before = 0, all = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFullMask, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < N / 32; ++w) {
-    const int s = warp_sums[w];
-    before += w < warp ? s : 0;
-    all += s;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const int n = warp_sums[w];
+      before += w < warp ? n : 0;
+      all += n;
+    }
+    if (t < p.n_tiles) prefix[t] = total + before + inc - v;
+    total += all;
   }
-  *total = all;
-  return before + inc - v;
+  if (threadIdx.x == 0) prefix[p.n_tiles] = total;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int t = threadIdx.x; t <= p.n_tiles; t += THREADS) p.prefix[t] = prefix[t];
+  return total;
 }
 
-// rows: of a tile, 8 or 16
+// rows: of a tile; 8 or 16 (stream), 128 or 256 (tile)
 cudaError_t launch_attend_stream(const AttendParams& p, int D, int rows, bool f16, int grid, cudaStream_t stream);
+// u16: every 16 positions from a multiple of 16 on share their scales
+cudaError_t launch_attend_tile(const AttendParams& p, int D, int rows, bool u16, bool f16, int grid,
+                               cudaStream_t stream);
 cudaError_t launch_attend_join(const AttendParams& p, int D, int rows, bool f16, cudaStream_t stream);
 int attend_stream_ctas_per_sm(int rows);
 
-constexpr int kMaxSplitTiles = 255;  // tiles of a launch whose CTAs share units
+constexpr int kMaxSplitTiles = 255;   // tiles of a launch whose CTAs share units: stream
+constexpr int kMaxSplitTiles2 = 2047; // tile
 
 }  // namespace hwr

@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
   if (p.n_ctas == 0) {
     // one CTA per (tile, head); the last tiles of a causal sequence, which see most, first
     const int t = p.n_tiles - 1 - blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads;
-    const Tile x = tile_at<R>(p, t);
+    const Tile x = tile_at(p, t, R);
     if (x.rows <= 0) return;
     segment<D, NT, F16>(p, x, h, 0, tile_units<kUnit>(x), true, 0, smem);
     return;
@@ -453,19 +453,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
   // Equal shares of all units, tile by tile and head by head.
   __shared__ int prefix[kMaxSplitTiles + 1];
   __shared__ int warp_sums[kWarps];
-  int total = 0;
-  for (int t0 = 0; t0 < p.n_tiles; t0 += kWarps * 32) {
-    const int t = t0 + threadIdx.x;
-    const int u = t < p.n_tiles ? tile_units<kUnit>(tile_at<R>(p, t)) : 0;
-    int all;
-    const int before = block_scan_tiles<kWarps * 32>(u, &all, warp_sums);
-    if (t < p.n_tiles) prefix[t] = total + before;
-    total += all;
-  }
-  if (threadIdx.x == 0) prefix[p.n_tiles] = total;
-  __syncthreads();
-  if (blockIdx.x == 0)
-    for (int t = threadIdx.x; t <= p.n_tiles; t += kWarps * 32) p.prefix[t] = prefix[t];
+  const int total = tile_prefix<kUnit, kWarps * 32>(p, R, prefix, warp_sums);
   const int64_t units = static_cast<int64_t>(total) * p.c.heads;
   const int64_t n = min(units, static_cast<int64_t>(p.n_ctas));
   if (blockIdx.x >= n) return;
@@ -473,27 +461,18 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
   const int64_t end = share_start(blockIdx.x + 1, units, n);
   bool first = true;
   while (u < end) {
-    int lo = 0, hi = p.n_tiles - 1;  // the last tile that starts at or before u (empty ones start with the next)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(prefix[mid]) * p.c.heads <= u) lo = mid; else hi = mid - 1;
-    }
-    const int tu = prefix[lo + 1] - prefix[lo];
-    const int64_t in = u - static_cast<int64_t>(prefix[lo]) * p.c.heads;
-    const int h = static_cast<int>(in / tu), u0 = static_cast<int>(in % tu);
-    const int u1 = static_cast<int>(min(static_cast<int64_t>(tu), u0 + (end - u)));
-    const Tile x = tile_at<R>(p, lo);
-    segment<D, NT, F16>(p, x, h, u0, u1, u0 == 0 && u1 == tu, 2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1),
-                        smem);
+    const Piece g = piece_at(p, prefix, u, end);
+    segment<D, NT, F16>(p, tile_at(p, g.tile, R), g.h, g.u0, g.u1, g.whole,
+                        2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1), smem);
     first = false;
-    u += u1 - u0;
+    u += g.u1 - g.u0;
   }
 }
 
 // Joins the parts of the (tile, head)s that several CTAs shared, in the order
 // of their keys.
-template <int D, int R, bool F16>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p) {
+template <int D, bool F16>
+__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int R) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int t = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads;
   const int base = p.prefix[t], tu = p.prefix[t + 1] - base;
@@ -504,7 +483,7 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   const int64_t c0 = share_owner(u0, units, n), c1 = share_owner(u0 + tu - 1, units, n);
   if (c0 == c1) return;
   const int64_t first = 2 * c0 + (share_start(c0, units, n) == u0 ? 0 : 1);
-  const Tile x = tile_at<R>(p, t);
+  const Tile x = tile_at(p, t, R);
   constexpr int kPer = D / 4;  // threads of a row
   const int d = (threadIdx.x % kPer) * 4;
   for (int i = blockIdx.y * (128 / kPer) + threadIdx.x / kPer; i < x.rows; i += gridDim.y * (128 / kPer)) {
@@ -539,10 +518,10 @@ cudaError_t go_stream(const AttendParams& p, int grid, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <int D, int R, bool F16>
-cudaError_t go_join(const AttendParams& p, cudaStream_t stream) {
+template <int D, bool F16>
+cudaError_t go_join(const AttendParams& p, int R, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles) * p.c.heads, R / 8);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles) * p.c.heads, R <= 16 ? R / 8 : R / 16);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -550,7 +529,7 @@ cudaError_t go_join(const AttendParams& p, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, R, F16>, p);
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<D, F16>, p, R);
 }
 
 }  // namespace
@@ -569,14 +548,8 @@ cudaError_t launch_attend_stream(const AttendParams& p, int D, int rows, bool f1
 }
 
 cudaError_t launch_attend_join(const AttendParams& p, int D, int rows, bool f16, cudaStream_t stream) {
-#define HWR_GO(DD, RR) return f16 ? go_join<DD, RR, true>(p, stream) : go_join<DD, RR, false>(p, stream)
-  if (D == 128) {
-    if (rows == 8) HWR_GO(128, 8);
-    HWR_GO(128, 16);
-  }
-  if (rows == 8) HWR_GO(64, 8);
-  HWR_GO(64, 16);
-#undef HWR_GO
+  if (D == 128) return f16 ? go_join<128, true>(p, rows, stream) : go_join<128, false>(p, rows, stream);
+  return f16 ? go_join<64, true>(p, rows, stream) : go_join<64, false>(p, rows, stream);
 }
 
 }  // namespace hwr

@@ -1,0 +1,796 @@
+// attend_tile.cu -- attention over the 8-bit cache for many query rows per
+// key/value head (prefill chunks, drafts, one query of a large group): tiles of
+// 128 rows x 128 keys on the fifth-generation tensor cores.
+//
+// Two streams of tiles run side by side in a CTA, so that one's softmax hides
+// the other's products: NM = 2, the two halves of 256 rows over the same keys;
+// NM = 1, the same 128 rows over alternate key tiles, joined at the end.
+//   warps 0-7   softmax, four a stream, a thread a row: scores from TMEM, weights
+//               back to TMEM as FP16; outputs at the end of a segment
+//   warps 8-15  fill: read codes, write them as FP16 (exact) in the swizzled
+//               layout of the products' operands, with the tokens' scales
+//   warp 16     issues the products, S = Q K^T and O += P V, P from TMEM
+// The arithmetic is that of attend.cuh: scales act on the FP32 scores, so the
+// operands are bare codes and a row's query scaled by a power of two.  The
+// reference of a row's exponentials rises only when a score exceeds it by
+// kSlack, which is rare after the first tile; then the row's outputs are
+// rescaled in TMEM.
+#include "attend.cuh"
+#include "internal.h"
+
+namespace hwr {
+namespace {
+
+constexpr int kSoftThreads = 256;
+constexpr int kFillWarps = 8;
+constexpr int kThreads = kSoftThreads + kFillWarps * 32 + 128;
+constexpr int kKeys = 128;                     // keys of a tile: a unit
+constexpr int kPanel = 128 * 128;              // bytes of 128 rows of 64 FP16
+constexpr int kScaleRing = 4;
+constexpr int kSoftBar = 1;
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
+constexpr uint32_t kTmemCols = 512;
+
+// Registers a thread: the block starts with kLaunchRegs (65,536 / 640, in whole
+// eights), and the three shares come to no more than that.
+constexpr int kLaunchRegs = 96;
+template <int NM>
+struct Regs {
+  static constexpr int kSoft = NM == 2 ? 144 : 120, kFill = NM == 2 ? 80 : 104, kIssue = 32;
+  static_assert(kSoftThreads * kSoft + kFillWarps * 32 * kFill + 128 * kIssue <= kThreads * kLaunchRegs, "");
+};
+
+template <int N>
+__device__ __forceinline__ void regs_to() {  // (down to more than there are, or up to fewer, is no valid instruction)
+  if constexpr (N > kLaunchRegs)
+    regs_up<N>();
+  else
+    regs_down<N>();
+}
+
+struct Bars {
+  uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
+  uint64_t sfull[2], pfull[2];  // by stream
+  uint64_t qfull, ofull, done, left;
+  uint32_t tmem;
+  int abort;
+};
+
+// Dynamic shared memory, from a 1,024-byte boundary.
+template <int D, int NM>
+struct Lay {
+  static constexpr int kPanels = D / 64;
+  static constexpr int kKV = kPanels * kPanel;   // a K or V tile
+  static constexpr int kQ = 0;                   // [NM][kPanels] panels; the exchange of NM = 1
+  static constexpr int kK = kQ + NM * kKV;       // [2]
+  static constexpr int kV = kK + 2 * kKV;        // [2]
+  static constexpr int kScale = kV + 2 * kKV;    // [kScaleRing][3][128]: key scale, log2 value scale, 1 / value scale
+  static constexpr int kNan = kScale + kScaleRing * 3 * 128 * 4;  // [2][128][4]: NaN codes of V tokens, a bit a dimension
+  static constexpr int kNanAny = kNan + 2 * 128 * 16;             // [2][8]: a word a fill warp, not 0 where it has any
+  static constexpr int kRowNan = kNanAny + 64;                    // [256][4]: dimensions made NaN, by row
+  static constexpr int kFactor = kRowNan + 256 * 16;              // [256]
+  static constexpr int kMl = kFactor + 1024;                      // [128] float2
+  static constexpr int kBars = kMl + 1024;
+  static constexpr int kPrefix = kBars + 256;                     // [kMaxSplitTiles2 + 1] and 17 sums
+  static constexpr int kBytes = kPrefix + (kMaxSplitTiles2 + 1) * 4 + 128 + 1024;
+};
+static_assert(sizeof(Bars) <= 256, "");
+
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t cvt_lo(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w)); }
+__device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16)); }
+// 0xFF in each byte of w that is a NaN code (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
+
+// A wait that, once it has run out, makes every further wait of the CTA end at
+// once: the loops then run through on whatever the buffers hold, all within
+// bounds, and the rows become NaN.
+__device__ __forceinline__ void wait(Bars* b, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
+  if (!mbar_wait(bar, parity, &b->abort, kWaitLimitNs)) *reinterpret_cast<volatile int*>(&b->abort) = 1;
+}
+
+// What a segment is: keys [128 u0, 128 u1) of (tile, head).
+struct Segment {
+  Tile x;          // (not for the issuing role)
+  int h, u0, n;
+  bool whole;
+  int64_t part;
+};
+
+// ------------------------------------------------------------------- fill --
+template <int D>
+struct Codes {
+  static constexpr int kN = D / 32;  // 16-byte pieces of a lane: 16 tokens of a warp
+  uint4 k[kN], v[kN];
+  float ks, vs;
+  uint32_t off;    // of token lane % 16
+  uint32_t valid;  // bit t: token t is one
+};
+
+template <int D>
+__device__ __forceinline__ void load_codes(const uint8_t* base, uint32_t off, uint32_t valid, uint4 (&r)[D / 32]) {
+  constexpr int kCh = D / 16, kRowsPer = 32 / kCh;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int t = i * kRowsPer + lane / kCh;
+    const uint32_t o = __shfl_sync(kFullMask, off, t);
+    r[i] = (valid >> t & 1) ? ldg_stream(base + (static_cast<int64_t>(o) << 4)) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Writes 16 tokens' codes as FP16 rows of 64 dimensions, chunks of 16 bytes at
+// (chunk ^ row % 8).  The upper half of a row's lanes writes its two chunks in
+// the other order, so that eight lanes never meet in a bank.
+template <int D, bool NANS>
+__device__ __forceinline__ void store_codes(uint32_t dst, const uint4 (&r)[D / 32], uint8_t* nan, uint32_t* nan_any) {
+  constexpr int kCh = D / 16, kRowsPer = 32 / kCh;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7, ch = lane % kCh;
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int t = warp * 16 + i * kRowsPer + lane / kCh;
+    uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+    if (NANS) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t nb = nan_bytes(w[e]);
+        w[e] &= ~nb;
+        bits |= ((nb & 1u) | (nb >> 7 & 2u) | (nb >> 14 & 4u) | (nb >> 21 & 8u)) << (4 * e);
+      }
+      *reinterpret_cast<uint16_t*>(nan + t * 16 + ch * 2) = static_cast<uint16_t>(bits);
+      any |= bits;
+    }
+    const bool sw = D == 128 && (ch & 4);
+    const uint32_t a0 = sw ? w[2] : w[0], a1 = sw ? w[3] : w[1], b0 = sw ? w[0] : w[2], b1 = sw ? w[1] : w[3];
+    const uint32_t row = dst + (ch >> 2) * kPanel + t * 128;
+    const int c0 = ((ch & 3) * 2 + (sw ? 1 : 0)) ^ (t & 7);
+    sts128(row + (c0 << 4), cvt_lo(a0), cvt_hi(a0), cvt_lo(a1), cvt_hi(a1));
+    sts128(row + ((c0 ^ 1) << 4), cvt_lo(b0), cvt_hi(b0), cvt_lo(b1), cvt_hi(b1));
+  }
+  if (NANS) {
+    any = __any_sync(kFullMask, any != 0);
+    if (lane == 0) *nan_any = any;
+  }
+}
+
+// tiles: tiles filled before the segment
+template <int D, int NM, bool U16>
+__device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, uint8_t* smem, uint32_t tiles) {
+  using L = Lay<D, NM>;
+  constexpr int kAhead = NM == 1 ? 2 : 1;  // tiles whose codes are on the way
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7, ch = lane % (D / 16);
+  const uint8_t* kbase = p.c.k + (g.h * p.c.head16 + ch) * 16;
+  const uint8_t* vbase = p.c.v + (g.h * p.c.head16 + ch) * 16;
+  Translate tr(p, g.x, g.h, min(g.x.n_keys, (g.u0 + g.n) * kKeys));
+  const int e0 = g.u0 * kKeys + warp * 16 + (lane & 15);
+  auto entry = [&](int j) { return e0 + j * kKeys; };
+  const int first_limit = p.sel_width ? INT32_MAX : row_limit(p, g.x, g.x.first);
+  Codes<D> c[kAhead];
+  auto take = [&](Codes<D>& d, const Translate::Scale& s) {
+    d.ks = s.ks, d.vs = s.vs, d.off = s.off16;
+    d.valid = __ballot_sync(kFullMask, s.pos != INT32_MAX);
+  };
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    take(c[a], tr.scale(tr.page(tr.index(entry(a)))));
+    load_codes<D>(kbase, c[a].off, c[a].valid, c[a].k);
+    load_codes<D>(vbase, c[a].off, c[a].valid, c[a].v);
+  }
+  Translate::Page pg = tr.page(tr.index(entry(kAhead)));
+  Translate::Index ix = tr.index(entry(kAhead + 1));
+  for (int j0 = 0; j0 < g.n; j0 += kAhead) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int j = j0 + a;
+      if (j >= g.n) break;
+      Codes<D>& d = c[a];
+      const uint32_t t = tiles + j, slot = t & 1, parity = (t >> 1 & 1) ^ 1;
+      const Translate::Scale s = tr.scale(pg);
+      pg = tr.page(ix);
+      ix = tr.index(entry(j + kAhead + 2));
+      wait(bars, &bars->kempty[slot], parity);
+      store_codes<D, false>(smem_u32(smem) + L::kK + slot * L::kKV, d.k, nullptr, nullptr);
+      float* sc = reinterpret_cast<float*>(smem + L::kScale) + (t & (kScaleRing - 1)) * 384;
+      if (U16 ? lane == 0 : lane < 16) {
+        const int at = U16 ? warp : warp * 16 + lane;
+        const bool on = d.valid >> (lane & 15) & 1;
+        const float lvs = on ? __log2f(fmaxf(d.vs, kMinBlockScale)) : -INFINITY;
+        sc[at] = on ? d.ks : 0.f;
+        sc[128 + at] = lvs;
+        sc[256 + at] = on ? ex2(-lvs) : 0.f;
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->kfull[slot]);
+      const Codes<D> old = d;
+      take(d, s);
+      load_codes<D>(kbase, d.off, d.valid, d.k);
+      wait(bars, &bars->vempty[slot], parity);
+      // Tokens that some rows see and others do not: a NaN among their values
+      // must not reach the latter as 0 * NaN, so it is noted beside the tile.
+      const uint32_t vdst = smem_u32(smem) + L::kV + slot * L::kKV;
+      if ((g.u0 + j + 1) * kKeys > first_limit)
+        store_codes<D, true>(vdst, old.v, smem + L::kNan + slot * (128 * 16),
+                             reinterpret_cast<uint32_t*>(smem + L::kNanAny) + slot * 8 + warp);
+      else
+        store_codes<D, false>(vdst, old.v, nullptr, nullptr);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->vfull[slot]);
+      load_codes<D>(vbase, d.off, d.valid, d.v);
+    }
+  }
+}
+
+// --------------------------------------------------------------- products --
+// One thread.  tiles: as above; phases: bit w, the parity of the tiles that stream w has had.
+template <int D, int NM>
+__device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, uint32_t& phases,
+                                         uint32_t segs) {
+  using L = Lay<D, NM>;
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  const uint32_t tm = bars->tmem, base = smem_u32(smem);
+  constexpr uint32_t kScoreDesc = idesc_f16<128, kKeys, false>(), kValueDesc = idesc_f16<128, D, true>();
+  // (an address advances its descriptor by a sixteenth of itself)
+  const uint64_t q0 = sw128_desc(base + L::kQ), k0 = sw128_desc(base + L::kK), v0 = sw128_mn_desc(base + L::kV, kPanel);
+  auto score = [&](int w, int i) {
+    const uint64_t q = q0 + (NM == 2 ? w * (L::kKV >> 4) : 0), k = k0 + ((tiles + i) & 1) * (L::kKV >> 4);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const uint32_t at = ((s >> 2) * kPanel + (s & 3) * 32) >> 4;
+      tc_mma_f16(tm + w * 128, q + at, k + at, kScoreDesc, s > 0);
+    }
+    tc_commit(&bars->sfull[w]);
+  };
+  auto value = [&](int w, int i, bool first) {
+    const uint64_t v = v0 + ((tiles + i) & 1) * (L::kKV >> 4);
+#pragma unroll
+    for (int s = 0; s < kKeys / 16; ++s)
+      tc_mma_f16_ts(tm + 256 + w * 128, tm + w * 128 + 64 + s * 8, v + s * (2048 >> 4), kValueDesc, !(first && s == 0));
+  };
+  auto kready = [&](int i) { wait(bars, &bars->kfull[(tiles + i) & 1], (tiles + i) >> 1 & 1); };
+  auto vready = [&](int i) { wait(bars, &bars->vfull[(tiles + i) & 1], (tiles + i) >> 1 & 1); };
+  auto pready = [&](int w) {
+    wait(bars, &bars->pfull[w], phases >> w & 1);
+    phases ^= 1u << w;
+    tc_fence_after();
+  };
+  wait(bars, &bars->qfull, segs & 1);
+  tc_fence_after();
+  if (NM == 2) {
+    kready(0);
+    score(0, 0);
+    score(1, 0);
+    tc_commit(&bars->kempty[tiles & 1]);
+    for (int i = 0; i < n; ++i) {
+      vready(i);
+      pready(0);
+      value(0, i, i == 0);
+      if (i + 1 < n) {
+        kready(i + 1);
+        score(0, i + 1);
+      }
+      pready(1);
+      value(1, i, i == 0);
+      tc_commit(&bars->vempty[(tiles + i) & 1]);
+      if (i + 1 < n) {
+        score(1, i + 1);
+        tc_commit(&bars->kempty[(tiles + i + 1) & 1]);
+      }
+    }
+  } else {
+    for (int i = 0; i < min(n, 2); ++i) {
+      kready(i);
+      score(i, i);
+      tc_commit(&bars->kempty[(tiles + i) & 1]);
+    }
+    for (int i = 0; i < n; ++i) {
+      const int w = i & 1;
+      vready(i);
+      pready(w);
+      value(w, i, i < 2);
+      tc_commit(&bars->vempty[(tiles + i) & 1]);
+      if (i + 2 < n) {
+        kready(i + 2);
+        score(w, i + 2);
+        tc_commit(&bars->kempty[(tiles + i) & 1]);
+      }
+    }
+  }
+  tc_commit(&bars->ofull);
+}
+
+// ---------------------------------------------------------------- softmax --
+// Query rows to shared memory, scaled by a power of two (and the sign of the
+// score scale, so that a larger product is a larger score).
+template <int D, int NM>
+__device__ __forceinline__ void load_q(const AttendParams& p, const Segment& g, uint8_t* smem, bool f16) {
+  using L = Lay<D, NM>;
+  constexpr int kPer = D / 8, kPass = kSoftThreads / kPer;  // threads of a row, rows of a pass
+  const int lane = threadIdx.x & 31, c = lane % kPer, sub = lane / kPer;
+  const float sign = p.scale_log2 < 0.f ? -1.f : 1.f, mag = fabsf(p.scale_log2);
+  constexpr int kU = 4;
+  for (int rw = (threadIdx.x >> 5) * (32 / kPer); rw < g.x.rows; rw += kU * kPass) {
+    const int r0 = rw + sub;
+    uint4 raw[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int r = r0 + u * kPass, pair = g.x.first + r;
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (r < g.x.rows)
+        raw[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (g.x.q0 + pair / p.G) * p.q_stride +
+                                                      (g.h * p.G + pair % p.G) * (2 * D)) + c);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int r = r0 + u * kPass;
+      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      float2 f[4];
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        f[e] = f16 ? unpack_act<true>(w[e]) : unpack_act<false>(w[e]);
+        m = fmaxf(m, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
+      }
+#pragma unroll
+      for (int o = kPer / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+      const float s = f16 ? 1.f : row_pow2(m), inv = sign / s;
+      if (r >= g.x.rows) continue;
+      sts128(smem_u32(smem) + L::kQ + (r >> 7) * L::kKV + (c >> 3) * kPanel + (r & 127) * 128 +
+                 (((c & 7) ^ (r & 7)) << 4),
+             half2_of(f[0].x * inv, f[0].y * inv), half2_of(f[1].x * inv, f[1].y * inv),
+             half2_of(f[2].x * inv, f[2].y * inv), half2_of(f[3].x * inv, f[3].y * inv));
+      if (c == 0) reinterpret_cast<float*>(smem + L::kFactor)[r] = s * mag;
+    }
+  }
+}
+
+struct Row {
+  float m, l;      // reference, and the sum
+  float factor;
+  int limit;       // positions that the row sees
+  int warp_limit;  // the least of its warp's
+};
+
+// Scales of 16 columns from `at` on.
+__device__ __forceinline__ float4 lds_f4(const float* s, int at) { return *reinterpret_cast<const float4*>(s + at); }
+
+// Largest score, in base 2 and with the value's scale, of 32 columns.
+template <bool U16, bool MASKED>
+__device__ __forceinline__ float top_of(const uint32_t (&r)[32], int c, const float* sc, const Row& row, int see,
+                                        float top) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int col = c * 32 + q * 16;
+    if (U16) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float s = __uint_as_float(r[q * 16 + e]);
+        m = fmaxf(m, !MASKED || col + e < see ? s : -INFINITY);
+      }
+      top = fmaxf(top, fmaf(m, sc[col / 16] * row.factor, sc[128 + col / 16]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 ks = lds_f4(sc, col + e), lv = lds_f4(sc + 128, col + e);
+        const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = fmaf(__uint_as_float(r[q * 16 + e + i]), k4[i] * row.factor, v4[i]);
+          top = fmaxf(top, !MASKED || col + e + i < see ? u : -INFINITY);
+        }
+      }
+    }
+  }
+  return top;
+}
+
+// Weights of 32 columns to TMEM, and their share of the row's sum.
+template <bool U16, bool MASKED>
+__device__ __forceinline__ void weights_of(const uint32_t (&r)[32], int c, const float* sc, Row& row, int see,
+                                           uint32_t dst) {
+  const float ref = row.m == -INFINITY ? 0.f : row.m - kHead;
+  uint32_t out[16];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int col = c * 32 + q * 16;
+    float2 sum = make_float2(0.f, 0.f);
+    float kf = 0.f, c0 = 0.f;
+    if (U16) kf = sc[col / 16] * row.factor, c0 = sc[128 + col / 16] - ref;
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      float4 ks, lv, iv;
+      if (!U16) ks = lds_f4(sc, col + e), lv = lds_f4(sc + 128, col + e), iv = lds_f4(sc + 256, col + e);
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const float2 s = make_float2(__uint_as_float(r[q * 16 + e + i]), __uint_as_float(r[q * 16 + e + i + 1]));
+        float2 k2 = make_float2(kf, kf), c2 = make_float2(c0, c0);
+        if (!U16) {
+          k2 = mul2(i ? make_float2(ks.z, ks.w) : make_float2(ks.x, ks.y), make_float2(row.factor, row.factor));
+          c2 = add2(i ? make_float2(lv.z, lv.w) : make_float2(lv.x, lv.y), make_float2(-ref, -ref));
+        }
+        const float2 u = fma2(s, k2, c2);
+        float2 w = make_float2(ex2(u.x), ex2(u.y));
+        if (MASKED) {
+          if (col + e + i >= see) w.x = 0.f;
+          if (col + e + i + 1 >= see) w.y = 0.f;
+        }
+        if (U16)
+          sum = add2(sum, w);
+        else
+          sum = fma2(w, i ? make_float2(iv.z, iv.w) : make_float2(iv.x, iv.y), sum);
+        out[q * 8 + (e + i) / 2] = half2_of(w.x, w.y);
+      }
+    }
+    row.l = U16 ? fmaf(sum.x + sum.y, sc[256 + col / 16], row.l) : row.l + (sum.x + sum.y);
+  }
+  tmem_st_x16(dst, out);
+}
+
+// One tile of a stream: its weights, and the rise of its rows' references.
+// tm_s, tm_o: the warp's lanes of the stream's scores and outputs; fresh: no
+// output yet.
+template <int D, bool U16, bool MASKED>
+__device__ __forceinline__ void softmax_tile(uint32_t tm_s, uint32_t tm_o, const float* sc, Row& row, int see,
+                                             bool fresh) {
+  // The weights go to the upper half of the scores' columns, so the second pass
+  // runs backwards: a piece overwrites only what has been read, and the last
+  // two pieces of the first pass are still in registers.
+  uint32_t a[32], b[32];
+  tmem_ld_x32(tm_s, a);
+  tmem_wait_ld(a);
+  tmem_ld_x32(tm_s + 32, b);
+  float top = top_of<U16, MASKED>(a, 0, sc, row, see, -INFINITY);
+  tmem_wait_ld(b);
+  tmem_ld_x32(tm_s + 64, a);
+  top = top_of<U16, MASKED>(b, 1, sc, row, see, top);
+  tmem_wait_ld(a);
+  tmem_ld_x32(tm_s + 96, b);
+  top = top_of<U16, MASKED>(a, 2, sc, row, see, top);
+  tmem_wait_ld(b);
+  top = top_of<U16, MASKED>(b, 3, sc, row, see, top);
+  if (__any_sync(kFullMask, top > row.m + kSlack)) {
+    const float m = fmaxf(row.m, top), f = m == row.m ? 1.f : ex2(row.m - m);
+    row.m = m;
+    row.l *= f;
+    if (!fresh) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t o[16];
+        tmem_ld_x16(tm_o + i * 16, o);
+        tmem_wait_ld(o);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st_x16(tm_o + i * 16, o);
+      }
+    }
+  }
+  weights_of<U16, MASKED>(b, 3, sc, row, see, tm_s + 64 + 48);
+  tmem_ld_x32(tm_s + 32, b);
+  weights_of<U16, MASKED>(a, 2, sc, row, see, tm_s + 64 + 32);
+  tmem_wait_ld(b);
+  tmem_ld_x32(tm_s, a);
+  weights_of<U16, MASKED>(b, 1, sc, row, see, tm_s + 64 + 16);
+  tmem_wait_ld(a);
+  weights_of<U16, MASKED>(a, 0, sc, row, see, tm_s + 64);
+  tmem_wait_st();
+}
+
+// 32 output columns of a row.
+__device__ __forceinline__ void store_out(const AttendParams& p, const Segment& g, int D, int rows, int i, int col,
+                                          const float (&o)[32], const Row& row, uint32_t nan, bool f16) {
+  const bool none = row.m == -INFINITY;
+  if (g.whole) {
+    const int pair = g.x.first + i;
+    const int64_t at = (g.x.q0 + pair / p.G) * static_cast<int64_t>(p.Hq) + g.h * p.G + pair % p.G;
+    const float inv = none ? 0.f : 1.f / row.l;
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float lo = nan >> (2 * e) & 1 ? NAN : o[2 * e] * inv, hi = nan >> (2 * e + 1) & 1 ? NAN : o[2 * e + 1] * inv;
+      w[e] = f16 ? pack_act<true>(lo, hi) : pack_act<false>(lo, hi);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(p.out + (at * D + col) * 2);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+    if (p.lse && col == 0) p.lse[at] = none ? -INFINITY : kLn2 * (row.m - kHead + log2f(row.l));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(p.part_o + (g.part * rows + i) * D + col);
+    float v[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = nan >> e & 1 ? NAN : o[e];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+    if (col == 0) p.part_ml[g.part * rows + i] = make_float2(row.m, row.l);
+  }
+}
+
+template <int D, int NM, bool U16>
+__device__ __forceinline__ void softmax(const AttendParams& p, const Segment& g, uint8_t* smem, uint32_t tiles,
+                                        uint32_t& count, uint32_t segs, bool f16) {
+  using L = Lay<D, NM>;
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  const int w = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31, first = t & ~31;
+  load_q<D, NM>(p, g, smem, f16);
+  uint32_t* row_nan = reinterpret_cast<uint32_t*>(smem + L::kRowNan) + threadIdx.x * 4;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) row_nan[e] = 0;
+  fence_async_smem();
+  named_bar(kSoftBar, kSoftThreads);
+  if (lane == 0) mbar_arrive(&bars->qfull);
+
+  const int r0 = NM == 2 ? w * 128 : 0;        // the stream's first row of the tile
+  const int i = min(r0 + t, g.x.rows - 1);     // (a row beyond the last repeats it; nothing of it is stored)
+  const bool busy = r0 + first < g.x.rows;     // of the warp's rows, one at least is one
+  Row row;
+  row.m = -INFINITY, row.l = 0.f;
+  row.factor = reinterpret_cast<const float*>(smem + L::kFactor)[i];
+  row.limit = p.sel_width ? INT32_MAX : row_limit(p, g.x, g.x.first + i);
+  row.warp_limit = p.sel_width ? INT32_MAX : row_limit(p, g.x, g.x.first + min(r0 + first, g.x.rows - 1));
+  const uint32_t lanes = static_cast<uint32_t>(first) << 16, tm = bars->tmem + lanes;
+  const uint32_t tm_s = tm + w * 128, tm_o = tm + 256 + w * 128;
+  constexpr int kEvery = NM == 2 ? 1 : 2;
+  for (int j = NM == 2 ? 0 : w; j < g.n; j += kEvery) {
+    wait(bars, &bars->sfull[w], count & 1);
+    ++count;
+    tc_fence_after();
+    if (busy) {
+      const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + ((tiles + j) & (kScaleRing - 1)) * 384;
+      const int pos0 = (g.u0 + j) * kKeys;
+      const bool fresh = j < kEvery;
+      if (pos0 + kKeys > row.warp_limit) {
+        const int see = max(min(row.limit - pos0, kKeys), 0);
+        softmax_tile<D, U16, true>(tm_s, tm_o, sc, row, see, fresh);
+        const uint32_t slot = (tiles + j) & 1;
+        wait(bars, &bars->vfull[slot], (tiles + j) >> 1 & 1);
+        const uint32_t* any = reinterpret_cast<const uint32_t*>(smem + L::kNanAny) + slot * 8;
+        uint32_t nans = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) nans |= any[e];
+        if (nans) {
+          const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + L::kNan) + slot * (128 * 4);
+          for (int k = 0; k < see; ++k)
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) row_nan[e] |= bits[k * 4 + e];
+        }
+      } else {
+        softmax_tile<D, U16, false>(tm_s, tm_o, sc, row, kKeys, fresh);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->pfull[w]);
+  }
+
+  wait(bars, &bars->ofull, segs & 1);
+  tc_fence_after();
+  if (*reinterpret_cast<volatile int*>(&bars->abort)) row.l = NAN;
+  if (isnan(row.l)) row.m = 0.f;  // a row of NaN scores counts in a join
+  constexpr int kRows = NM * 128;
+  if (NM == 2) {
+    if (busy) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld_x32(tm_o + c * 32, r);
+        tmem_wait_ld(r);
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]);
+        if (r0 + t < g.x.rows) store_out(p, g, D, kRows, r0 + t, c * 32, o, row, row_nan[c], f16);
+      }
+    }
+    return;
+  }
+  // NM = 1: the second stream hands its rows over, 32 columns at a time, in the
+  // queries' place (the products that read them are done).
+  float2* ml = reinterpret_cast<float2*>(smem + L::kMl);
+  uint8_t* ex = smem + L::kQ + t * 128;
+  if (w == 1) ml[t] = make_float2(row.m, row.l);
+  const uint32_t* other_nan = row_nan + 128 * 4;
+  float f0 = 1.f, f1 = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t r[32];
+    if (busy) {
+      tmem_ld_x32(tm_o + c * 32, r);
+      tmem_wait_ld(r);
+    }
+    if (w == 1 && busy) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        *reinterpret_cast<uint4*>(ex + ((e ^ (t & 7)) << 4)) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+    }
+    named_bar(kSoftBar, kSoftThreads);
+    if (w == 0 && busy) {
+      if (c == 0) {
+        const float2 o = ml[t];
+        const float m = fmaxf(row.m, o.x);
+        f0 = row.m == -INFINITY ? 0.f : ex2(row.m - m);
+        f1 = o.x == -INFINITY ? 0.f : ex2(o.x - m);
+        row.l = (f0 == 0.f ? 0.f : f0 * row.l) + (f1 == 0.f ? 0.f : f1 * o.y);
+        row.m = m;
+      }
+      float o[32];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 v = *reinterpret_cast<const float4*>(ex + ((e ^ (t & 7)) << 4));
+        const float b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[4 * e + k] = (f0 == 0.f ? 0.f : f0 * __uint_as_float(r[4 * e + k])) + (f1 == 0.f ? 0.f : f1 * b[k]);
+      }
+      if (t < g.x.rows) store_out(p, g, D, kRows, t, c * 32, o, row, row_nan[c] | other_nan[c], f16);
+    }
+    named_bar(kSoftBar, kSoftThreads);
+  }
+}
+
+// ----------------------------------------------------------------- kernel --
+template <int D, int NM, bool U16>
+__global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ AttendParams p, int f16) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  using L = Lay<D, NM>;
+  constexpr int R = NM * 128;
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  int* prefix = reinterpret_cast<int*>(smem + L::kPrefix);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // The CTA's share of the units, or its one (tile, head): where it starts, and
+  // its units.
+  int tile, h, u0;
+  int64_t share;
+  if (p.n_ctas) {
+    const int total = tile_prefix<kKeys, kThreads>(p, R, prefix, prefix + kMaxSplitTiles2 + 1);
+    const int64_t units = static_cast<int64_t>(total) * p.c.heads, n = min(units, static_cast<int64_t>(p.n_ctas));
+    if (blockIdx.x >= n) return;
+    const int64_t u = share_start(blockIdx.x, units, n), end = share_start(blockIdx.x + 1, units, n);
+    const Piece c = piece_at(p, prefix, u, end);
+    tile = c.tile, h = c.h, u0 = c.u0, share = end - u;
+  } else {
+    tile = p.n_tiles - 1 - blockIdx.x / p.c.heads;  // those of a sequence that see most, first
+    h = blockIdx.x % p.c.heads, u0 = 0;
+    const Tile x = tile_at(p, tile, R);
+    if (x.rows <= 0) return;
+    share = tile_units<kKeys>(x);
+    if (threadIdx.x == 0) prefix[tile & 1] = 0, prefix[(tile & 1) + 1] = static_cast<int>(share);
+    prefix += (tile & 1) - tile;  // prefix[tile], prefix[tile + 1]
+  }
+  if (warp == 16) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars->kfull[i], kFillWarps);
+        mbar_init(&bars->vfull[i], kFillWarps);
+        mbar_init(&bars->kempty[i], 1);
+        mbar_init(&bars->vempty[i], 1);
+        mbar_init(&bars->sfull[i], 1);
+        mbar_init(&bars->pfull[i], 4);
+      }
+      mbar_init(&bars->qfull, kSoftThreads / 32);
+      mbar_init(&bars->ofull, 1);
+      mbar_init(&bars->done, 1);
+      mbar_init(&bars->left, kSoftThreads / 32);
+      bars->abort = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(&bars->tmem, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  // Each role goes through the segments of the share by itself, and ends by
+  // itself: registers are divided among them, so no code but this follows that
+  // several of them run, and the two with few call no function (a division of
+  // 64 bits is one).
+  const int tile_first = tile, h_first = h, u_first = u0;
+  auto each = [&](bool with_tile, auto&& role) {
+    uint32_t tiles = 0, segs = 0;
+    int64_t left = share;
+    int t = tile_first, hh = h_first, at = u_first;
+    while (left > 0) {
+      const int units = prefix[t + 1] - prefix[t];
+      if (at >= units) {  // the next head, or tile
+        at = 0;
+        if (units == 0 || ++hh == p.c.heads) ++t, hh = 0;
+        continue;
+      }
+      Segment g;
+      if (with_tile) g.x = tile_at(p, t, R);
+      g.h = hh, g.u0 = at;
+      g.n = static_cast<int>(min(static_cast<int64_t>(units - at), left));
+      g.whole = g.n == units;
+      g.part = 2 * static_cast<int64_t>(blockIdx.x) + (segs ? 1 : 0);
+      role(g, tiles, segs);
+      tiles += g.n, at += g.n, left -= g.n;
+      ++segs;
+    }
+  };
+  if (warp < 8) {
+    regs_to<Regs<NM>::kSoft>();
+    uint32_t count = 0;
+    each(true, [&](const Segment& g, uint32_t tiles, uint32_t segs) {
+      softmax<D, NM, U16>(p, g, smem, tiles, count, segs, f16);
+    });
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->left);
+    return;
+  }
+  if (warp < 16) {
+    regs_to<Regs<NM>::kFill>();
+    each(true, [&](const Segment& g, uint32_t tiles, uint32_t) { fill<D, NM, U16>(p, g, smem, tiles); });
+    return;
+  }
+  regs_to<Regs<NM>::kIssue>();
+  if (warp != 16) return;
+  uint32_t gone = 1;
+  if (lane == 0) {
+    uint32_t phases = 0;
+    each(false, [&](const Segment& g, uint32_t tiles, uint32_t segs) { products<D, NM>(g.n, smem, tiles, phases, segs); });
+    // All products have completed and all softmax warps have left before TMEM is
+    // freed: these waits end by a time limit alone, and then it stays allocated.
+    tc_commit(&bars->done);
+    gone = mbar_wait(&bars->done, 0u, nullptr, kWaitLimitNs) && mbar_wait(&bars->left, 0u, nullptr, kWaitLimitNs);
+    if (p.status && (bars->abort || !gone)) atomicOr(p.status, kStatusWaitTimeout);
+  }
+  gone = __shfl_sync(kFullMask, gone, 0);
+  tc_fence_after();
+  if (gone) tmem_dealloc(bars->tmem, kTmemCols);
+}
+
+template <int D, int NM, bool U16>
+cudaError_t go_tile(const AttendParams& p, bool f16, int grid, cudaStream_t stream) {
+  // (at least half of an SM's: one CTA an SM, since each takes all of its TMEM)
+  constexpr int kBytes = Lay<D, NM>::kBytes > 118784 ? Lay<D, NM>::kBytes : 118784;
+  static_assert(kBytes <= 232448, "");
+  // The shares of registers presume those of the launch: with fewer, the waits for
+  // more would not end.
+  static const bool regs_ok = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, attend_tile_kernel<D, NM, U16>) == cudaSuccess && a.numRegs == kLaunchRegs;
+  }();
+  if (!regs_ok) return cudaErrorInvalidConfiguration;
+  const cudaError_t e =
+      cudaFuncSetAttribute(attend_tile_kernel<D, NM, U16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e != cudaSuccess) return e;
+  attend_tile_kernel<D, NM, U16><<<grid, kThreads, kBytes, stream>>>(p, f16 ? 1 : 0);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tile(const AttendParams& p, int D, int rows, bool u16, bool f16, int grid,
+                               cudaStream_t stream) {
+#define HWR_GO(DD, NN) return u16 ? go_tile<DD, NN, true>(p, f16, grid, stream) : go_tile<DD, NN, false>(p, f16, grid, stream)
+  if (D == 128) {
+    if (rows == 128) HWR_GO(128, 1);
+    HWR_GO(128, 2);
+  }
+  if (rows == 128) HWR_GO(64, 1);
+  HWR_GO(64, 2);
+#undef HWR_GO
+}
+
+}  // namespace hwr

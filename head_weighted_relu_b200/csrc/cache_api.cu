@@ -75,7 +75,7 @@ indexer_status view_seqs(const indexer_sequences* s, bool pointers, SeqView* v) 
 struct AttendPlan {
   AttendParams p;
   bool f16;
-  int D, rows;   // rows of a tile
+  int D, rows;   // rows of a tile: up to 16, the streaming kernel
   int grid;
   size_t off_prefix, off_ml, off_o, bytes;
 };
@@ -108,17 +108,19 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   // rows that share a pass over the keys: of a query with a selection, of a
   // sequence without
   const int64_t most_rows = a->sel_width ? p.G : static_cast<int64_t>(a->max_q ? a->max_q : s->S) * p.G;
-  const int R = pl->rows = most_rows <= 8 ? 8 : 16;
+  const int R = pl->rows = most_rows <= 8 ? 8 : most_rows <= 16 ? 16 : most_rows <= 128 ? 128 : 256;
   p.sel_tiles = (p.G + R - 1) / R;
   const int64_t tiles = a->sel_width ? s->S * p.sel_tiles : s->S * p.G / R + s->B;
   const int64_t items = tiles * c->heads;
   if (items > INT32_MAX - 1024) return INDEXER_EUNSUPPORTED;
   p.n_tiles = static_cast<int32_t>(tiles);
-  const int slots = sms * attend_stream_ctas_per_sm(R);
+  const bool stream = R <= 16;
+  const int slots = stream ? sms * attend_stream_ctas_per_sm(R) : sms;
   // Fewer (tile, head)s than fill the SMs a few times over: the CTAs share all
   // keys equally, across tiles, and a second kernel joins the parts.
   const int64_t most_keys = a->sel_width ? a->sel_width : p.max_keys;
-  const bool split = tiles <= kMaxSplitTiles && items < 8 * slots && tiles * (most_keys / 64 + 1) <= INT32_MAX;
+  const bool split = tiles <= (stream ? kMaxSplitTiles : kMaxSplitTiles2) && items < 8 * slots &&
+                     tiles * (most_keys / 64 + 1) <= INT32_MAX;
   p.n_ctas = split ? slots : 0;
   pl->grid = split ? slots : static_cast<int>(items);
   size_t at = 0;
@@ -238,7 +240,10 @@ indexer_status indexer_cache_attend(const indexer_cache* cache, const indexer_se
   p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + pl.off_o);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (launch_attend_stream(p, pl.D, pl.rows, pl.f16, pl.grid, cs) != cudaSuccess) return INDEXER_ECUDA;
+  const bool u16 = !p.sel_width && p.c.block % 16 == 0;
+  const cudaError_t e = pl.rows <= 16 ? launch_attend_stream(p, pl.D, pl.rows, pl.f16, pl.grid, cs)
+                                      : launch_attend_tile(p, pl.D, pl.rows, u16, pl.f16, pl.grid, cs);
+  if (e != cudaSuccess) return INDEXER_ECUDA;
   if (p.n_ctas && launch_attend_join(p, pl.D, pl.rows, pl.f16, cs) != cudaSuccess) return INDEXER_ECUDA;
   return INDEXER_OK;
 }
