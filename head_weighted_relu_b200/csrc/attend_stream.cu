@@ -469,42 +469,73 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
   }
 }
 
-// Joins the parts of the (tile, head)s that several CTAs shared, in the order
-// of their keys.
+// Joins the parts of the (tile, head)s that several CTAs shared, in the order of
+// their keys: block x takes the one that begins in CTA x's share and goes on in
+// the next, if there is one.  Eight groups of threads take every eighth part of
+// the same rows, so that a row of many parts is not one long chain of loads.
+constexpr int kJoinGroups = 8;
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p, int R) {
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p, int R) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.x / p.c.heads, h = blockIdx.x % p.c.heads;
-  const int base = p.prefix[t], tu = p.prefix[t + 1] - base;
-  if (tu == 0) return;
   const int64_t units = static_cast<int64_t>(p.prefix[p.n_tiles]) * p.c.heads;
-  const int64_t u0 = static_cast<int64_t>(base) * p.c.heads + static_cast<int64_t>(h) * tu;
   const int64_t n = min(units, static_cast<int64_t>(p.n_ctas));
-  const int64_t c0 = share_owner(u0, units, n), c1 = share_owner(u0 + tu - 1, units, n);
-  if (c0 == c1) return;
-  const int64_t first = 2 * c0 + (share_start(c0, units, n) == u0 ? 0 : 1);
-  const Tile x = tile_at(p, t, R);
-  constexpr int kPer = D / 4;  // threads of a row
-  const int d = (threadIdx.x % kPer) * 4;
-  for (int i = blockIdx.y * (128 / kPer) + threadIdx.x / kPer; i < x.rows; i += gridDim.y * (128 / kPer)) {
-    float m = -INFINITY;
-    for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, p.part_ml[(c == c0 ? first : 2 * c) * R + i].x);
-    float l = 0.f, o[4] = {};
+  if (blockIdx.x + 1 >= n) return;
+  const int64_t start = share_start(blockIdx.x, units, n), end = share_start(blockIdx.x + 1, units, n);
+  const Piece g = piece_at(p, p.prefix, end - 1, end);
+  const int tu = p.prefix[g.tile + 1] - p.prefix[g.tile];
+  const int64_t u0 = static_cast<int64_t>(p.prefix[g.tile]) * p.c.heads + static_cast<int64_t>(g.h) * tu;
+  if (g.u0 + 1 == tu || u0 < start) return;  // complete, or begun in an earlier share
+  const int c0 = blockIdx.x, parts = static_cast<int>(share_owner(u0 + tu - 1, units, n)) - c0 + 1;
+  const int64_t first = 2 * static_cast<int64_t>(c0) + (u0 == start ? 0 : 1);
+  const Tile x = tile_at(p, g.tile, R);
+  constexpr int kPer = D / 4, kRows = 256 / kJoinGroups / kPer > 0 ? 256 / kJoinGroups / kPer : 1;
+  static_assert(kRows * kPer * kJoinGroups == 256, "");
+  __shared__ float4 sum[kJoinGroups][kRows][kPer];
+  __shared__ float2 ml[kJoinGroups][kRows];
+  const int d = threadIdx.x % kPer, sub = threadIdx.x / kPer % kRows, group = threadIdx.x / (kPer * kRows);
+  for (int i0 = blockIdx.y * kRows; i0 < x.rows; i0 += gridDim.y * kRows) {
+    const int i = i0 + sub;
+    const bool on = i < x.rows;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
 #pragma unroll 4
-    for (int64_t c = c0; c <= c1; ++c) {
-      const int64_t at = (c == c0 ? first : 2 * c) * R + i;
-      const float2 v = p.part_ml[at];
-      const float4 a = *reinterpret_cast<const float4*>(p.part_o + at * D + d);
-      const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
-      l += f * v.y;
-      if (f != 0.f) o[0] += f * a.x, o[1] += f * a.y, o[2] += f * a.z, o[3] += f * a.w;
+      for (int c = group; c < parts; c += kJoinGroups)
+        m = fmaxf(m, p.part_ml[(c == 0 ? first : 2 * static_cast<int64_t>(c0 + c)) * R + i].x);
+#pragma unroll 4
+      for (int c = group; c < parts; c += kJoinGroups) {
+        const int64_t at = (c == 0 ? first : 2 * static_cast<int64_t>(c0 + c)) * R + i;
+        const float2 v = p.part_ml[at];
+        const float4 a = *reinterpret_cast<const float4*>(p.part_o + at * D + d * 4);
+        const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
+        l += f * v.y;
+        if (f != 0.f) o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
+      }
     }
-    const int pair = x.first + i;
-    const int64_t at = (x.q0 + pair / p.G) * static_cast<int64_t>(p.Hq) + h * p.G + pair % p.G;
-    const float inv = m == -INFINITY ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.out + (at * D + d) * 2) =
-        make_uint2(pack_act<F16>(o[0] * inv, o[1] * inv), pack_act<F16>(o[2] * inv, o[3] * inv));
-    if (p.lse && d == 0) p.lse[at] = m == -INFINITY ? -INFINITY : kLn2 * (m - kHead + log2f(l));
+    sum[group][sub][d] = o;
+    if (d == 0) ml[group][sub] = make_float2(m, l);
+    __syncthreads();
+    if (on && group == 0) {
+#pragma unroll
+      for (int k = 1; k < kJoinGroups; ++k) m = fmaxf(m, ml[k][sub].x);
+      l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < kJoinGroups; ++k) {
+        const float2 v = ml[k][sub];
+        const float4 a = sum[k][sub][d];
+        const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
+        l += f * v.y;
+        if (f != 0.f) o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
+      }
+      const int pair = x.first + i;
+      const int64_t at = (x.q0 + pair / p.G) * static_cast<int64_t>(p.Hq) + g.h * p.G + pair % p.G;
+      const float inv = m == -INFINITY ? 0.f : 1.f / l;
+      *reinterpret_cast<uint2*>(p.out + (at * D + d * 4) * 2) =
+          make_uint2(pack_act<F16>(o.x * inv, o.y * inv), pack_act<F16>(o.z * inv, o.w * inv));
+      if (p.lse && d == 0) p.lse[at] = m == -INFINITY ? -INFINITY : kLn2 * (m - kHead + log2f(l));
+    }
+    __syncthreads();
   }
 }
 
@@ -521,8 +552,8 @@ cudaError_t go_stream(const AttendParams& p, int grid, cudaStream_t stream) {
 template <int D, bool F16>
 cudaError_t go_join(const AttendParams& p, int R, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_tiles) * p.c.heads, R <= 16 ? R / 8 : R / 16);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_ctas), R <= 16 ? R / 4 : 32);
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

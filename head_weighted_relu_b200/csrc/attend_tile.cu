@@ -70,7 +70,8 @@ struct Lay {
   static constexpr int kRowNan = kNanAny + 64;                    // [256][4]: dimensions made NaN, by row
   static constexpr int kFactor = kRowNan + 256 * 16;              // [256]
   static constexpr int kMl = kFactor + 1024;                      // [128] float2
-  static constexpr int kBars = kMl + 1024;
+  static constexpr int kSeg = kMl + 1024;                         // [2] the softmax warps' Segment
+  static constexpr int kBars = kSeg + 256;
   static constexpr int kPrefix = kBars + 256;                     // [kMaxSplitTiles2 + 1] and 17 sums
   static constexpr int kBytes = kPrefix + (kMaxSplitTiles2 + 1) * 4 + 128 + 1024;
 };
@@ -97,10 +98,16 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w &
 
 // A wait that, once it has run out, makes every further wait of the CTA end at
 // once: the loops then run through on whatever the buffers hold, all within
-// bounds, and the rows become NaN.
+// bounds, and the rows become NaN.  (A try suspends the thread for about a
+// microsecond, so the limit is some seconds.)
+constexpr int kWaitTries = 1 << 22;
 __device__ __forceinline__ void wait(Bars* b, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return;
-  if (!mbar_wait(bar, parity, &b->abort, kWaitLimitNs)) *reinterpret_cast<volatile int*>(&b->abort) = 1;
+#pragma unroll 1
+  for (int i = 0; !mbar_try_wait(bar, parity); ++i)
+    if (i >= kWaitTries || *reinterpret_cast<volatile int*>(&b->abort)) {
+      *reinterpret_cast<volatile int*>(&b->abort) = 1;
+      return;
+    }
 }
 
 // What a segment is: keys [128 u0, 128 u1) of (tile, head).
@@ -112,24 +119,33 @@ struct Segment {
 };
 
 // ------------------------------------------------------------------- fill --
+// A fill warp has 16 tokens of each tile.  Where 16 positions share their page
+// and scales (U16), one look-up serves them, and `off` is that of the first
+// and `valid` their number; otherwise lane t looks up token t, and `valid` has
+// a bit for each.
 template <int D>
 struct Codes {
-  static constexpr int kN = D / 32;  // 16-byte pieces of a lane: 16 tokens of a warp
+  static constexpr int kN = D / 32;  // 16-byte pieces of a lane
   uint4 k[kN], v[kN];
   float ks, vs;
-  uint32_t off;    // of token lane % 16
-  uint32_t valid;  // bit t: token t is one
+  uint32_t off, valid;
 };
 
-template <int D>
-__device__ __forceinline__ void load_codes(const uint8_t* base, uint32_t off, uint32_t valid, uint4 (&r)[D / 32]) {
+template <int D, bool U16>
+__device__ __forceinline__ void load_codes(const uint8_t* base, uint32_t row16, uint32_t off, uint32_t valid,
+                                           uint4 (&r)[D / 32]) {
   constexpr int kCh = D / 16, kRowsPer = 32 / kCh;
   const int lane = threadIdx.x & 31;
+  const uint8_t* at = base + (static_cast<int64_t>(off) << 4);
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     const int t = i * kRowsPer + lane / kCh;
-    const uint32_t o = __shfl_sync(kFullMask, off, t);
-    r[i] = (valid >> t & 1) ? ldg_stream(base + (static_cast<int64_t>(o) << 4)) : make_uint4(0, 0, 0, 0);
+    if (U16) {  // base: of the lane's row
+      r[i] = t < valid ? ldg_stream(at + static_cast<int64_t>(i) * row16 * (kRowsPer * 16)) : make_uint4(0, 0, 0, 0);
+    } else {
+      const uint32_t o = __shfl_sync(kFullMask, off, t);
+      r[i] = (valid >> t & 1) ? ldg_stream(base + (static_cast<int64_t>(o) << 4)) : make_uint4(0, 0, 0, 0);
+    }
   }
 }
 
@@ -176,22 +192,28 @@ __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, ui
   constexpr int kAhead = NM == 1 ? 2 : 1;  // tiles whose codes are on the way
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7, ch = lane % (D / 16);
-  const uint8_t* kbase = p.c.k + (g.h * p.c.head16 + ch) * 16;
-  const uint8_t* vbase = p.c.v + (g.h * p.c.head16 + ch) * 16;
-  Translate tr(p, g.x, g.h, min(g.x.n_keys, (g.u0 + g.n) * kKeys));
-  const int e0 = g.u0 * kKeys + warp * 16 + (lane & 15);
+  const int64_t lane0 = (g.h * p.c.head16 + ch + (U16 ? lane / (D / 16) * p.c.token16 : 0)) * 16;
+  const uint8_t* kbase = p.c.k + lane0;
+  const uint8_t* vbase = p.c.v + lane0;
+  const uint32_t row16 = static_cast<uint32_t>(p.c.token16);
+  const int end = min(g.x.n_keys, (g.u0 + g.n) * kKeys);
+  Translate tr(p, g.x, g.h, end);
+  const int e0 = g.u0 * kKeys + warp * 16 + (U16 ? 0 : lane & 15);
   auto entry = [&](int j) { return e0 + j * kKeys; };
   const int first_limit = p.sel_width ? INT32_MAX : row_limit(p, g.x, g.x.first);
   Codes<D> c[kAhead];
   auto take = [&](Codes<D>& d, const Translate::Scale& s) {
     d.ks = s.ks, d.vs = s.vs, d.off = s.off16;
-    d.valid = __ballot_sync(kFullMask, s.pos != INT32_MAX);
+    if (U16)
+      d.valid = s.pos == INT32_MAX ? 0 : min(end - s.pos, 16);
+    else
+      d.valid = __ballot_sync(kFullMask, s.pos != INT32_MAX);
   };
 #pragma unroll
   for (int a = 0; a < kAhead; ++a) {
     take(c[a], tr.scale(tr.page(tr.index(entry(a)))));
-    load_codes<D>(kbase, c[a].off, c[a].valid, c[a].k);
-    load_codes<D>(vbase, c[a].off, c[a].valid, c[a].v);
+    load_codes<D, U16>(kbase, row16, c[a].off, c[a].valid, c[a].k);
+    load_codes<D, U16>(vbase, row16, c[a].off, c[a].valid, c[a].v);
   }
   Translate::Page pg = tr.page(tr.index(entry(kAhead)));
   Translate::Index ix = tr.index(entry(kAhead + 1));
@@ -210,7 +232,7 @@ __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, ui
       float* sc = reinterpret_cast<float*>(smem + L::kScale) + (t & (kScaleRing - 1)) * 384;
       if (U16 ? lane == 0 : lane < 16) {
         const int at = U16 ? warp : warp * 16 + lane;
-        const bool on = d.valid >> (lane & 15) & 1;
+        const bool on = U16 ? d.valid > 0 : d.valid >> (lane & 15) & 1;
         const float lvs = on ? __log2f(fmaxf(d.vs, kMinBlockScale)) : -INFINITY;
         sc[at] = on ? d.ks : 0.f;
         sc[128 + at] = lvs;
@@ -221,7 +243,7 @@ __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, ui
       if (lane == 0) mbar_arrive(&bars->kfull[slot]);
       const Codes<D> old = d;
       take(d, s);
-      load_codes<D>(kbase, d.off, d.valid, d.k);
+      load_codes<D, U16>(kbase, row16, d.off, d.valid, d.k);
       wait(bars, &bars->vempty[slot], parity);
       // Tokens that some rows see and others do not: a NaN among their values
       // must not reach the latter as 0 * NaN, so it is noted beside the tile.
@@ -234,7 +256,7 @@ __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, ui
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->vfull[slot]);
-      load_codes<D>(vbase, d.off, d.valid, d.v);
+      load_codes<D, U16>(vbase, row16, d.off, d.valid, d.v);
     }
   }
 }
@@ -248,22 +270,28 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const uint32_t tm = bars->tmem, base = smem_u32(smem);
   constexpr uint32_t kScoreDesc = idesc_f16<128, kKeys, false>(), kValueDesc = idesc_f16<128, D, true>();
-  // (an address advances its descriptor by a sixteenth of itself)
-  const uint64_t q0 = sw128_desc(base + L::kQ), k0 = sw128_desc(base + L::kK), v0 = sw128_mn_desc(base + L::kV, kPanel);
+  // (an address advances its descriptor's low word by a sixteenth of itself)
+  const uint64_t qd = sw128_desc(base + L::kQ), kd = sw128_desc(base + L::kK), vd = sw128_mn_desc(base + L::kV, kPanel);
+  constexpr uint32_t kHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+  const uint32_t q0 = static_cast<uint32_t>(qd), k0 = static_cast<uint32_t>(kd), v0 = static_cast<uint32_t>(vd);
+  auto desc = [](uint32_t lo) { return static_cast<uint64_t>(kHi) << 32 | lo; };
   auto score = [&](int w, int i) {
-    const uint64_t q = q0 + (NM == 2 ? w * (L::kKV >> 4) : 0), k = k0 + ((tiles + i) & 1) * (L::kKV >> 4);
-#pragma unroll
+    uint32_t q = q0 + (NM == 2 ? w * (L::kKV >> 4) : 0), k = k0 + ((tiles + i) & 1) * (L::kKV >> 4);
+    asm volatile("" : "+r"(q), "+r"(k));  // (or every step's descriptors are kept through the loop)
+#pragma unroll 1
     for (int s = 0; s < D / 16; ++s) {
       const uint32_t at = ((s >> 2) * kPanel + (s & 3) * 32) >> 4;
-      tc_mma_f16(tm + w * 128, q + at, k + at, kScoreDesc, s > 0);
+      tc_mma_f16(tm + w * 128, desc(q + at), desc(k + at), kScoreDesc, s > 0);
     }
     tc_commit(&bars->sfull[w]);
   };
   auto value = [&](int w, int i, bool first) {
-    const uint64_t v = v0 + ((tiles + i) & 1) * (L::kKV >> 4);
-#pragma unroll
+    uint32_t v = v0 + ((tiles + i) & 1) * (L::kKV >> 4);
+    asm volatile("" : "+r"(v));
+#pragma unroll 1
     for (int s = 0; s < kKeys / 16; ++s)
-      tc_mma_f16_ts(tm + 256 + w * 128, tm + w * 128 + 64 + s * 8, v + s * (2048 >> 4), kValueDesc, !(first && s == 0));
+      tc_mma_f16_ts(tm + 256 + w * 128, tm + w * 128 + s * 8, desc(v + s * (2048 >> 4)), kValueDesc,
+                    !(first && s == 0));
   };
   auto kready = [&](int i) { wait(bars, &bars->kfull[(tiles + i) & 1], (tiles + i) >> 1 & 1); };
   auto vready = [&](int i) { wait(bars, &bars->vfull[(tiles + i) & 1], (tiles + i) >> 1 & 1); };
@@ -451,29 +479,26 @@ __device__ __forceinline__ void weights_of(const uint32_t (&r)[32], int c, const
 template <int D, bool U16, bool MASKED>
 __device__ __forceinline__ void softmax_tile(uint32_t tm_s, uint32_t tm_o, const float* sc, Row& row, int see,
                                              bool fresh) {
-  // The weights go to the upper half of the scores' columns, so the second pass
-  // runs backwards: a piece overwrites only what has been read, and the last
-  // two pieces of the first pass are still in registers.
+  // The loops are not unrolled further: all roles' code together has to stay in
+  // the instruction cache (unrolled, the issuing warp waited for its own code).
   uint32_t a[32], b[32];
-  tmem_ld_x32(tm_s, a);
-  tmem_wait_ld(a);
-  tmem_ld_x32(tm_s + 32, b);
-  float top = top_of<U16, MASKED>(a, 0, sc, row, see, -INFINITY);
-  tmem_wait_ld(b);
-  tmem_ld_x32(tm_s + 64, a);
-  top = top_of<U16, MASKED>(b, 1, sc, row, see, top);
-  tmem_wait_ld(a);
-  tmem_ld_x32(tm_s + 96, b);
-  top = top_of<U16, MASKED>(a, 2, sc, row, see, top);
-  tmem_wait_ld(b);
-  top = top_of<U16, MASKED>(b, 3, sc, row, see, top);
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {
+    tmem_ld_x32(tm_s + c * 32, a);
+    tmem_ld_x32(tm_s + c * 32 + 32, b);
+    tmem_wait_ld(a);
+    tmem_wait_ld(b);
+    top = top_of<U16, MASKED>(a, c, sc, row, see, top);
+    top = top_of<U16, MASKED>(b, c + 1, sc, row, see, top);
+  }
   if (__any_sync(kFullMask, top > row.m + kSlack)) {
     const float m = fmaxf(row.m, top), f = m == row.m ? 1.f : ex2(row.m - m);
     row.m = m;
     row.l *= f;
     if (!fresh) {
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
+#pragma unroll 1
+      for (int i = 0; i < D / 16; ++i) {  // (rare)
         uint32_t o[16];
         tmem_ld_x16(tm_o + i * 16, o);
         tmem_wait_ld(o);
@@ -483,14 +508,17 @@ __device__ __forceinline__ void softmax_tile(uint32_t tm_s, uint32_t tm_o, const
       }
     }
   }
-  weights_of<U16, MASKED>(b, 3, sc, row, see, tm_s + 64 + 48);
-  tmem_ld_x32(tm_s + 32, b);
-  weights_of<U16, MASKED>(a, 2, sc, row, see, tm_s + 64 + 32);
-  tmem_wait_ld(b);
+  // A piece's weights take the place of half its scores, and of no later ones.
   tmem_ld_x32(tm_s, a);
-  weights_of<U16, MASKED>(b, 1, sc, row, see, tm_s + 64 + 16);
-  tmem_wait_ld(a);
-  weights_of<U16, MASKED>(a, 0, sc, row, see, tm_s + 64);
+#pragma unroll 1
+  for (int c = 0; c < 4; c += 2) {
+    tmem_wait_ld(a);
+    tmem_ld_x32(tm_s + c * 32 + 32, b);
+    weights_of<U16, MASKED>(a, c, sc, row, see, tm_s + c * 16);
+    tmem_wait_ld(b);
+    if (c == 0) tmem_ld_x32(tm_s + 64, a);
+    weights_of<U16, MASKED>(b, c + 1, sc, row, see, tm_s + c * 16 + 16);
+  }
   tmem_wait_st();
 }
 
@@ -524,12 +552,16 @@ __device__ __forceinline__ void store_out(const AttendParams& p, const Segment& 
 }
 
 template <int D, int NM, bool U16>
-__device__ __forceinline__ void softmax(const AttendParams& p, const Segment& g, uint8_t* smem, uint32_t tiles,
+__device__ __forceinline__ void softmax(const AttendParams& p, const Segment& seg, uint8_t* smem, uint32_t tiles,
                                         uint32_t& count, uint32_t segs, bool f16) {
   using L = Lay<D, NM>;
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int w = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31, first = t & ~31;
-  load_q<D, NM>(p, g, smem, f16);
+  static_assert(sizeof(Segment) <= 128, "");
+  load_q<D, NM>(p, seg, smem, f16);
+  // (the key loop has no registers for it)
+  const Segment& g = *reinterpret_cast<Segment*>(smem + L::kSeg + (segs & 1) * 128);
+  if (threadIdx.x == 0) *reinterpret_cast<Segment*>(smem + L::kSeg + (segs & 1) * 128) = seg;
   uint32_t* row_nan = reinterpret_cast<uint32_t*>(smem + L::kRowNan) + threadIdx.x * 4;
 #pragma unroll
   for (int e = 0; e < 4; ++e) row_nan[e] = 0;
@@ -548,13 +580,14 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& g,
   const uint32_t lanes = static_cast<uint32_t>(first) << 16, tm = bars->tmem + lanes;
   const uint32_t tm_s = tm + w * 128, tm_o = tm + 256 + w * 128;
   constexpr int kEvery = NM == 2 ? 1 : 2;
-  for (int j = NM == 2 ? 0 : w; j < g.n; j += kEvery) {
+  const int n = g.n, u0 = g.u0;
+  for (int j = NM == 2 ? 0 : w; j < n; j += kEvery) {
     wait(bars, &bars->sfull[w], count & 1);
     ++count;
     tc_fence_after();
     if (busy) {
       const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + ((tiles + j) & (kScaleRing - 1)) * 384;
-      const int pos0 = (g.u0 + j) * kKeys;
+      const int pos0 = (u0 + j) * kKeys;
       const bool fresh = j < kEvery;
       if (pos0 + kKeys > row.warp_limit) {
         const int see = max(min(row.limit - pos0, kKeys), 0);
