@@ -24,6 +24,14 @@ constexpr float kSlack = 8.f;   // a row's reference rises once it is exceeded b
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The (tile, head) that begins in a CTA's share and goes on in the next: its
+// parts are `first`, then the first part of each CTA that follows.
+struct JoinJob {
+  int64_t last, units;   // its last unit, of so many; last -1 for no such one
+  int32_t first;
+  int32_t rows, q0, pair, h;
+};
+
 struct AttendParams {
   CacheView c;
   SeqView s;
@@ -41,7 +49,7 @@ struct AttendParams {
   int32_t n_tiles;         // tile slots
   int32_t sel_tiles;       // tiles of one query (selection)
   int32_t n_ctas;          // CTAs that share the units, or 0: one CTA per (tile, head)
-  int32_t* prefix;         // [n_tiles + 1] unit counts before each tile (workspace)
+  JoinJob* jobs;           // [n_ctas] (workspace)
   float* part_o;           // [2 n_ctas][rows][D]
   float2* part_ml;         // [2 n_ctas][rows]: reference and sum
   uint32_t* status;
@@ -109,7 +117,7 @@ __device__ __forceinline__ int row_limit(const AttendParams& p, const Tile& x, i
 
 // prefix[t]: the units of the tiles before t, for one head; prefix[n_tiles]: of
 // all, which is returned.  For CTAs of THREADS threads that share a launch's
-// units; all take part.  CTA 0 leaves a copy in the workspace for the join.
+// units; all take part.
 template <int UNIT, int THREADS>
 __device__ __forceinline__ int tile_prefix(const AttendParams& p, int R, int* prefix, int* warp_sums);
 
@@ -124,12 +132,16 @@ struct Piece {
   int tile, h, u0, u1;
   bool whole;  // all of the (tile, head)'s units
 };
-__device__ __forceinline__ Piece piece_at(const AttendParams& p, const int* prefix, int64_t u, int64_t end) {
+__device__ __forceinline__ int tile_of(const AttendParams& p, const int* prefix, int64_t u) {
   int lo = 0, hi = p.n_tiles - 1;  // the last tile that starts at or before u (empty ones start with the next)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (static_cast<int64_t>(prefix[mid]) * p.c.heads <= u) lo = mid; else hi = mid - 1;
   }
+  return lo;
+}
+__device__ __forceinline__ Piece piece_at(const AttendParams& p, const int* prefix, int64_t u, int64_t end) {
+  const int lo = tile_of(p, prefix, u);
   const int tu = prefix[lo + 1] - prefix[lo];
   const int64_t in = u - static_cast<int64_t>(prefix[lo]) * p.c.heads;
   Piece r;
@@ -161,6 +173,7 @@ struct Translate {
 
   struct Index { int pos; };                              // position, or INT_MAX
   struct Page { int pos; int off; int page; };            // page: as loaded
+  struct Place { int pos; uint32_t off16; int64_t scale; };  // scale: index of its scales
   struct Scale { int pos; uint32_t off16; float ks, vs; };
 
   __device__ __forceinline__ Translate(const AttendParams& p_, const Tile& x_, int h_, int end_)
@@ -182,18 +195,25 @@ struct Translate {
     r.page = pi < p.s.table_pages ? __ldg(pages + pi) : -1;
     return r;
   }
-  __device__ __forceinline__ Scale scale(const Page& g) const {
-    Scale r{INT32_MAX, 0, 0.f, 1.f};
+  __device__ __forceinline__ Place place(const Page& g) const {
+    Place r{INT32_MAX, 0, 0};
     if (g.pos == INT32_MAX) return r;
     if (g.page < 0 || g.page >= p.c.n_pages) {
       if (p.status) atomicOr(p.status, kStatusToken);
       return r;
     }
-    const int64_t si = (static_cast<int64_t>(g.page) * p.c.page_blocks + (g.off >> p.c.block_shift)) * p.c.heads + h;
     r.pos = g.pos;
     r.off16 = static_cast<uint32_t>(g.page * p.c.page16 + g.off * p.c.token16);
-    r.ks = __ldg(p.c.ks + si);
-    r.vs = __ldg(p.c.vs + si);
+    r.scale = (static_cast<int64_t>(g.page) * p.c.page_blocks + (g.off >> p.c.block_shift)) * p.c.heads + h;
+    return r;
+  }
+  __device__ __forceinline__ Scale scale(const Page& g) const {
+    const Place a = place(g);
+    Scale r{a.pos, a.off16, 0.f, 1.f};
+    if (a.pos != INT32_MAX) {
+      r.ks = __ldg(p.c.ks + a.scale);
+      r.vs = __ldg(p.c.vs + a.scale);
+    }
     return r;
   }
   __device__ __forceinline__ TokenEntry entry(const Scale& s) const {
@@ -254,9 +274,25 @@ __device__ __forceinline__ int tile_prefix(const AttendParams& p, int R, int* pr
   }
   if (threadIdx.x == 0) prefix[p.n_tiles] = total;
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int t = threadIdx.x; t <= p.n_tiles; t += THREADS) p.prefix[t] = prefix[t];
   return total;
+}
+
+// Notes this CTA's job for the join; [start, end) is its share of `units`.  One thread.
+__device__ __forceinline__ void note_job(const AttendParams& p, int R, const int* prefix, int64_t units,
+                                         int64_t start, int64_t end) {
+  JoinJob j = {};
+  j.last = -1;
+  if (start < end) {
+    const int t = tile_of(p, prefix, end - 1), tu = prefix[t + 1] - prefix[t];
+    int64_t u0 = static_cast<int64_t>(prefix[t]) * p.c.heads;
+    int h = 0;
+    while (u0 + tu < end) u0 += tu, ++h;  // (a head at a time: no division, which would be a function)
+    if (u0 + tu > end && u0 >= start) {
+      const Tile x = tile_at(p, t, R);
+      j = JoinJob{u0 + tu - 1, units, static_cast<int>(2 * blockIdx.x) + (u0 == start ? 0 : 1), x.rows, x.q0, x.first, h};
+    }
+  }
+  p.jobs[blockIdx.x] = j;
 }
 
 // rows: of a tile; 8 or 16 (stream), 128 or 256 (tile)

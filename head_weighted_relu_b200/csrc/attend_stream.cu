@@ -456,9 +456,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
   const int total = tile_prefix<kUnit, kWarps * 32>(p, R, prefix, warp_sums);
   const int64_t units = static_cast<int64_t>(total) * p.c.heads;
   const int64_t n = min(units, static_cast<int64_t>(p.n_ctas));
-  if (blockIdx.x >= n) return;
-  int64_t u = share_start(blockIdx.x, units, n);
-  const int64_t end = share_start(blockIdx.x + 1, units, n);
+  int64_t u = 0, end = 0;
+  if (blockIdx.x < n) u = share_start(blockIdx.x, units, n), end = share_start(blockIdx.x + 1, units, n);
+  if (threadIdx.x == 0) note_job(p, R, prefix, units, u, end);
   bool first = true;
   while (u < end) {
     const Piece g = piece_at(p, prefix, u, end);
@@ -470,72 +470,82 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
 }
 
 // Joins the parts of the (tile, head)s that several CTAs shared, in the order of
-// their keys: block x takes the one that begins in CTA x's share and goes on in
-// the next, if there is one.  Eight groups of threads take every eighth part of
-// the same rows, so that a row of many parts is not one long chain of loads.
-constexpr int kJoinGroups = 8;
+// their keys: block x does CTA x's job.  A warp takes a row; of many parts,
+// the block's eight warps take a row together, every eighth part each, so that
+// it is not one long chain of loads.
+template <int D>
+__device__ __forceinline__ void add_parts(const AttendParams& p, int first, int parts, int R, int i, int c, int step,
+                                          int d, float& m, float& l, float (&o)[D / 32]) {
+  auto index = [&](int k) { return (k == 0 ? first : 2 * (static_cast<int64_t>(blockIdx.x) + k)) * R + i; };
+  m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int k = c; k < parts; k += step) m = fmaxf(m, __ldcg(&p.part_ml[index(k)]).x);
+#pragma unroll 4
+  for (int k = c; k < parts; k += step) {
+    const int64_t at = index(k);
+    const float2 v = __ldcg(&p.part_ml[at]);
+    float a[D / 32];
+    if (D == 128) {
+      const float4 w = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
+      a[0] = w.x, a[1] = w.y, a[D / 32 - 2] = w.z, a[D / 32 - 1] = w.w;
+    } else {
+      const float2 w = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D + d));
+      a[0] = w.x, a[1] = w.y;
+    }
+    const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
+    l += f * v.y;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e)
+      if (f != 0.f) o[e] += f * a[e];
+  }
+}
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p, int R) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t units = static_cast<int64_t>(p.prefix[p.n_tiles]) * p.c.heads;
-  const int64_t n = min(units, static_cast<int64_t>(p.n_ctas));
-  if (blockIdx.x + 1 >= n) return;
-  const int64_t start = share_start(blockIdx.x, units, n), end = share_start(blockIdx.x + 1, units, n);
-  const Piece g = piece_at(p, p.prefix, end - 1, end);
-  const int tu = p.prefix[g.tile + 1] - p.prefix[g.tile];
-  const int64_t u0 = static_cast<int64_t>(p.prefix[g.tile]) * p.c.heads + static_cast<int64_t>(g.h) * tu;
-  if (g.u0 + 1 == tu || u0 < start) return;  // complete, or begun in an earlier share
-  const int c0 = blockIdx.x, parts = static_cast<int>(share_owner(u0 + tu - 1, units, n)) - c0 + 1;
-  const int64_t first = 2 * static_cast<int64_t>(c0) + (u0 == start ? 0 : 1);
-  const Tile x = tile_at(p, g.tile, R);
-  constexpr int kPer = D / 4, kRows = 256 / kJoinGroups / kPer > 0 ? 256 / kJoinGroups / kPer : 1;
-  static_assert(kRows * kPer * kJoinGroups == 256, "");
-  __shared__ float4 sum[kJoinGroups][kRows][kPer];
-  __shared__ float2 ml[kJoinGroups][kRows];
-  const int d = threadIdx.x % kPer, sub = threadIdx.x / kPer % kRows, group = threadIdx.x / (kPer * kRows);
-  for (int i0 = blockIdx.y * kRows; i0 < x.rows; i0 += gridDim.y * kRows) {
-    const int i = i0 + sub;
-    const bool on = i < x.rows;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on) {
-#pragma unroll 4
-      for (int c = group; c < parts; c += kJoinGroups)
-        m = fmaxf(m, p.part_ml[(c == 0 ? first : 2 * static_cast<int64_t>(c0 + c)) * R + i].x);
-#pragma unroll 4
-      for (int c = group; c < parts; c += kJoinGroups) {
-        const int64_t at = (c == 0 ? first : 2 * static_cast<int64_t>(c0 + c)) * R + i;
-        const float2 v = p.part_ml[at];
-        const float4 a = *reinterpret_cast<const float4*>(p.part_o + at * D + d * 4);
+  const JoinJob g = p.jobs[blockIdx.x];
+  if (g.last < 0) return;
+  const int parts = static_cast<int>(share_owner(g.last, g.units, min(g.units, static_cast<int64_t>(p.n_ctas)))) -
+                    static_cast<int>(blockIdx.x) + 1;
+  constexpr int kN = D / 32, kWarps = 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = lane * kN;
+  const bool together = parts > kWarps;
+  __shared__ float sum[kWarps][D];
+  __shared__ float2 ml[kWarps];
+  for (int i = together ? blockIdx.y : blockIdx.y * kWarps + warp; i < g.rows; i += gridDim.y * (together ? 1 : kWarps)) {
+    float m, l, o[kN];
+    add_parts<D>(p, g.first, parts, R, i, together ? warp : 0, together ? kWarps : 1, d, m, l, o);
+    if (together) {  // (all warps have the same i)
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kN; ++e) sum[warp][d + e] = o[e];
+      if (lane == 0) ml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (warp != 0) continue;
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) m = fmaxf(m, ml[k].x);
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) {
+        const float2 v = ml[k];
         const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
         l += f * v.y;
-        if (f != 0.f) o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
+#pragma unroll
+        for (int e = 0; e < kN; ++e)
+          if (f != 0.f) o[e] += f * sum[k][d + e];
       }
     }
-    sum[group][sub][d] = o;
-    if (d == 0) ml[group][sub] = make_float2(m, l);
-    __syncthreads();
-    if (on && group == 0) {
+    const int pair = g.pair + i;
+    const int64_t at = (g.q0 + pair / p.G) * static_cast<int64_t>(p.Hq) + g.h * p.G + pair % p.G;
+    const float inv = m == -INFINITY ? 0.f : 1.f / l;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (at * D + d) * 2);
 #pragma unroll
-      for (int k = 1; k < kJoinGroups; ++k) m = fmaxf(m, ml[k][sub].x);
-      l = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kJoinGroups; ++k) {
-        const float2 v = ml[k][sub];
-        const float4 a = sum[k][sub][d];
-        const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
-        l += f * v.y;
-        if (f != 0.f) o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
-      }
-      const int pair = x.first + i;
-      const int64_t at = (x.q0 + pair / p.G) * static_cast<int64_t>(p.Hq) + g.h * p.G + pair % p.G;
-      const float inv = m == -INFINITY ? 0.f : 1.f / l;
-      *reinterpret_cast<uint2*>(p.out + (at * D + d * 4) * 2) =
-          make_uint2(pack_act<F16>(o.x * inv, o.y * inv), pack_act<F16>(o.z * inv, o.w * inv));
-      if (p.lse && d == 0) p.lse[at] = m == -INFINITY ? -INFINITY : kLn2 * (m - kHead + log2f(l));
-    }
-    __syncthreads();
+    for (int e = 0; e < kN; e += 2) dst[e / 2] = pack_act<F16>(o[e] * inv, o[e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[at] = m == -INFINITY ? -INFINITY : kLn2 * (m - kHead + log2f(l));
   }
 }
 
@@ -552,7 +562,7 @@ cudaError_t go_stream(const AttendParams& p, int grid, cudaStream_t stream) {
 template <int D, bool F16>
 cudaError_t go_join(const AttendParams& p, int R, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.n_ctas), R <= 16 ? R / 4 : 32);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.n_ctas), R <= 16 ? R : 32);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];

@@ -7,9 +7,11 @@
 // NM = 1, the same 128 rows over alternate key tiles, joined at the end.
 //   warps 0-7   softmax, four a stream, a thread a row: scores from TMEM, weights
 //               back to TMEM as FP16; outputs at the end of a segment
-//   warps 8-15  fill: read codes, write them as FP16 (exact) in the swizzled
-//               layout of the products' operands, with the tokens' scales
+//   warps 8-15  fill: read codes, keys and values four each, and write them as
+//               FP16 (exact) in the swizzled layout of the products' operands,
+//               with the tokens' scales
 //   warp 16     issues the products, S = Q K^T and O += P V, P from TMEM
+//   warps 17-19 look up the tokens of the tiles ahead
 // The arithmetic is that of attend.cuh: scales act on the FP32 scores, so the
 // operands are bare codes and a row's query scaled by a power of two.  The
 // reference of a row's exponentials rises only when a score exceeds it by
@@ -26,8 +28,7 @@ constexpr int kFillWarps = 8;
 constexpr int kThreads = kSoftThreads + kFillWarps * 32 + 128;
 constexpr int kKeys = 128;                     // keys of a tile: a unit
 constexpr int kPanel = 128 * 128;              // bytes of 128 rows of 64 FP16
-constexpr int kScaleRing = 4;
-constexpr int kSoftBar = 1;
+constexpr int kSoftBar = 1, kLookBar = 2;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;
 constexpr uint32_t kTmemCols = 512;
 
@@ -36,7 +37,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kLaunchRegs = 96;
 template <int NM>
 struct Regs {
-  static constexpr int kSoft = NM == 2 ? 144 : 120, kFill = NM == 2 ? 80 : 104, kIssue = 32;
+  static constexpr int kSoft = NM == 2 ? 144 : 112, kFill = NM == 2 ? 72 : 104, kIssue = 48;
   static_assert(kSoftThreads * kSoft + kFillWarps * 32 * kFill + 128 * kIssue <= kThreads * kLaunchRegs, "");
 };
 
@@ -52,30 +53,34 @@ struct Bars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t sfull[2], pfull[2];  // by stream
   uint64_t qfull, ofull, done, left;
+  uint64_t tfull[8], tempty[8];
   uint32_t tmem;
   int abort;
 };
 
 // Dynamic shared memory, from a 1,024-byte boundary.
-template <int D, int NM>
+template <int D, int NM, bool U16>
 struct Lay {
   static constexpr int kPanels = D / 64;
+  static constexpr int kEntries = U16 ? 8 : 128;  // look-ups of a tile
+  static constexpr int kRing = U16 || NM == 1 ? 8 : 4;  // tiles whose look-ups are kept
   static constexpr int kKV = kPanels * kPanel;   // a K or V tile
   static constexpr int kQ = 0;                   // [NM][kPanels] panels; the exchange of NM = 1
   static constexpr int kK = kQ + NM * kKV;       // [2]
   static constexpr int kV = kK + 2 * kKV;        // [2]
-  static constexpr int kScale = kV + 2 * kKV;    // [kScaleRing][3][128]: key scale, log2 value scale, 1 / value scale
-  static constexpr int kNan = kScale + kScaleRing * 3 * 128 * 4;  // [2][128][4]: NaN codes of V tokens, a bit a dimension
-  static constexpr int kNanAny = kNan + 2 * 128 * 16;             // [2][8]: a word a fill warp, not 0 where it has any
+  static constexpr int kScale = kV + 2 * kKV;    // [kRing][3][entries]: key scale, log2 value scale, 1 / value scale
+  static constexpr int kPlace = kScale + kRing * 3 * kEntries * 4;  // [kRing][entries]: place and number
+  static constexpr int kNan = kPlace + kRing * kEntries * 8;  // [2][128][4]: NaN codes of V tokens, a bit a dimension
+  static constexpr int kNanAny = kNan + 2 * 128 * 16;             // [2][4]: a word a value warp, not 0 where it has any
   static constexpr int kRowNan = kNanAny + 64;                    // [256][4]: dimensions made NaN, by row
   static constexpr int kFactor = kRowNan + 256 * 16;              // [256]
   static constexpr int kMl = kFactor + 1024;                      // [128] float2
   static constexpr int kSeg = kMl + 1024;                         // [2] the softmax warps' Segment
   static constexpr int kBars = kSeg + 256;
-  static constexpr int kPrefix = kBars + 256;                     // [kMaxSplitTiles2 + 1] and 17 sums
+  static constexpr int kPrefix = kBars + 320;                     // [kMaxSplitTiles2 + 1] and 17 sums
   static constexpr int kBytes = kPrefix + (kMaxSplitTiles2 + 1) * 4 + 128 + 1024;
 };
-static_assert(sizeof(Bars) <= 256, "");
+static_assert(sizeof(Bars) <= 320, "");
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
   uint4 v;
@@ -100,7 +105,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w &
 // once: the loops then run through on whatever the buffers hold, all within
 // bounds, and the rows become NaN.  (A try suspends the thread for about a
 // microsecond, so the limit is some seconds.)
-constexpr int kWaitTries = 1 << 22;
+constexpr int kWaitTries = 1 << 21;
 __device__ __forceinline__ void wait(Bars* b, uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
   for (int i = 0; !mbar_try_wait(bar, parity); ++i)
@@ -118,155 +123,186 @@ struct Segment {
   int64_t part;
 };
 
-// ------------------------------------------------------------------- fill --
-// A fill warp has 16 tokens of each tile.  Where 16 positions share their page
-// and scales (U16), one look-up serves them, and `off` is that of the first
-// and `valid` their number; otherwise lane t looks up token t, and `valid` has
-// a bit for each.
-template <int D>
-struct Codes {
-  static constexpr int kN = D / 32;  // 16-byte pieces of a lane
-  uint4 k[kN], v[kN];
-  float ks, vs;
-  uint32_t off, valid;
-};
-
-template <int D, bool U16>
-__device__ __forceinline__ void load_codes(const uint8_t* base, uint32_t row16, uint32_t off, uint32_t valid,
-                                           uint4 (&r)[D / 32]) {
-  constexpr int kCh = D / 16, kRowsPer = 32 / kCh;
-  const int lane = threadIdx.x & 31;
-  const uint8_t* at = base + (static_cast<int64_t>(off) << 4);
+// -------------------------------------------------------------- look-ups --
+// Three warps look up the tokens of the tiles ahead: their places for the fill
+// warps, their scales for the softmax.  Where 16 positions share their page and
+// scales (U16), an entry stands for 16 tokens: `off` is the place of the first
+// and `valid` their number; otherwise for one.
+template <int D, int NM, bool U16>
+__device__ __forceinline__ void look_up(const AttendParams& p, const Segment& g, uint8_t* smem, uint32_t tiles) {
+  using L = Lay<D, NM, U16>;
+  constexpr int kEntries = L::kEntries;
+  constexpr int kPer = U16 ? 1 : 4;    // of a lane
+  constexpr int kTiles = U16 ? 2 : 1;  // that a warp takes at once
+  static_assert(3 * kTiles <= L::kRing, "");
+  Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 17;
+  const int end = min(g.x.n_keys, (g.u0 + g.n) * kKeys);
+  const Translate tr(p, g.x, g.h, end);
+#pragma unroll 1
+  for (int j0 = 0; j0 < g.n; j0 += 3 * kTiles) {
+    const int j = j0 + warp * kTiles + (U16 ? lane >> 3 & 1 : 0), en = U16 ? lane & 7 : lane;
+    const bool on_lane = j < g.n && (!U16 || lane < 16);
+    const uint32_t slot = (tiles + j) % L::kRing, parity = ((tiles + j) / L::kRing & 1) ^ 1;
+    Translate::Index ix[kPer];
+    Translate::Page pg[kPer];
+    Translate::Place at[kPer];
+    float ks[kPer], vs[kPer];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int t = i * kRowsPer + lane / kCh;
-    if (U16) {  // base: of the lane's row
-      r[i] = t < valid ? ldg_stream(at + static_cast<int64_t>(i) * row16 * (kRowsPer * 16)) : make_uint4(0, 0, 0, 0);
-    } else {
-      const uint32_t o = __shfl_sync(kFullMask, off, t);
-      r[i] = (valid >> t & 1) ? ldg_stream(base + (static_cast<int64_t>(o) << 4)) : make_uint4(0, 0, 0, 0);
+    for (int e = 0; e < kPer; ++e) ix[e] = tr.index((g.u0 + j) * kKeys + (U16 ? en * 16 : e * 32 + en));
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) pg[e] = tr.page(ix[e]);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      at[e] = tr.place(pg[e]);
+      const bool on = at[e].pos != INT32_MAX;
+      ks[e] = on ? __ldg(p.c.ks + at[e].scale) : 0.f;
+      vs[e] = on ? __ldg(p.c.vs + at[e].scale) : 1.f;
+    }
+    if (on_lane) wait(bars, &bars->tempty[slot], parity);
+    __syncwarp();
+    if (on_lane) {
+      float* sc = reinterpret_cast<float*>(smem + L::kScale) + slot * (3 * kEntries);
+      uint2* place = reinterpret_cast<uint2*>(smem + L::kPlace) + slot * kEntries;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const int k = e * 32 + en;
+        const bool on = at[e].pos != INT32_MAX;
+        const float lvs = on ? __log2f(fmaxf(vs[e], kMinBlockScale)) : -INFINITY;
+        sc[k] = ks[e], sc[kEntries + k] = lvs, sc[2 * kEntries + k] = on ? ex2(-lvs) : 0.f;
+        place[k] = make_uint2(at[e].off16, on ? (U16 ? min(end - at[e].pos, 16) : 1) : 0);
+      }
+    }
+    __syncwarp();
+    if (on_lane && en == 0) mbar_arrive(&bars->tfull[slot]);
+    // A round, no longer than the ring, is complete before the next: a barrier's
+    // parity would not tell two laps apart.
+    named_bar(kLookBar, 96);
+  }
+}
+
+// ------------------------------------------------------------------- fill --
+// Four warps fill the keys' tiles and four the values', 32 tokens of each a warp.
+template <int D, bool U16>
+__device__ __forceinline__ void load_codes(const uint8_t* base, uint32_t row16, const uint2* place,
+                                           uint4 (&r)[D / 16]) {
+  constexpr int kCh = D / 16, kRowsPer = 32 / kCh;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    uint2 w;
+    if (U16) w = place[warp * 2 + g];
+    const uint8_t* at = base + (static_cast<int64_t>(w.x) << 4);  // (U16: base is of the lane's row)
+#pragma unroll
+    for (int i = 0; i < kCh / 2; ++i) {
+      const uint32_t t = i * kRowsPer + lane / kCh;
+      if (!U16) w = place[warp * 32 + g * 16 + t], at = base + (static_cast<int64_t>(w.x) << 4);
+      r[g * (kCh / 2) + i] = (U16 ? t : 0u) < w.y
+                                 ? ldg_stream(U16 ? at + static_cast<int64_t>(i * kRowsPer * 16) * row16 : at)
+                                 : make_uint4(0, 0, 0, 0);
     }
   }
 }
 
-// Writes 16 tokens' codes as FP16 rows of 64 dimensions, chunks of 16 bytes at
+// Writes 32 tokens' codes as FP16 rows of 64 dimensions, chunks of 16 bytes at
 // (chunk ^ row % 8).  The upper half of a row's lanes writes its two chunks in
 // the other order, so that eight lanes never meet in a bank.
-template <int D, bool NANS>
-__device__ __forceinline__ void store_codes(uint32_t dst, const uint4 (&r)[D / 32], uint8_t* nan, uint32_t* nan_any) {
+template <int D>
+__device__ __forceinline__ void store_codes(uint32_t dst, const uint4 (&r)[D / 16]) {
   constexpr int kCh = D / 16, kRowsPer = 32 / kCh;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7, ch = lane % kCh;
+  const int lane = threadIdx.x & 31, ch = lane % kCh, t0 = ((threadIdx.x >> 5) & 3) * 32 + lane / kCh;
+  const bool sw = D == 128 && (ch & 4);
+  dst += (ch >> 2) * kPanel + t0 * 128;
+  const int c0 = (ch & 3) * 2 + (sw ? 1 : 0);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const uint32_t a0 = sw ? r[i].z : r[i].x, a1 = sw ? r[i].w : r[i].y, b0 = sw ? r[i].x : r[i].z,
+                   b1 = sw ? r[i].y : r[i].w;
+    const uint32_t at = dst + i * kRowsPer * 128 + ((c0 ^ ((t0 + i * kRowsPer) & 7)) << 4);
+    sts128(at, cvt_lo(a0), cvt_hi(a0), cvt_lo(a1), cvt_hi(a1));
+    sts128(at ^ 16, cvt_lo(b0), cvt_hi(b0), cvt_lo(b1), cvt_hi(b1));
+  }
+}
+
+// Takes the NaN codes out of 32 tokens' values and notes them, a bit a dimension.
+template <int D>
+__device__ __forceinline__ void take_nans(uint4 (&r)[D / 16], uint8_t* nan, uint32_t* nan_any) {
+  constexpr int kCh = D / 16, kRowsPer = 32 / kCh;
+  const int lane = threadIdx.x & 31, ch = lane % kCh, t0 = ((threadIdx.x >> 5) & 3) * 32 + lane / kCh;
   uint32_t any = 0;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int t = warp * 16 + i * kRowsPer + lane / kCh;
-    uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-    if (NANS) {
-      uint32_t bits = 0;
+  for (int i = 0; i < D / 16; ++i) {
+    uint32_t* w[4] = {&r[i].x, &r[i].y, &r[i].z, &r[i].w};
+    uint32_t bits = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t nb = nan_bytes(w[e]);
-        w[e] &= ~nb;
-        bits |= ((nb & 1u) | (nb >> 7 & 2u) | (nb >> 14 & 4u) | (nb >> 21 & 8u)) << (4 * e);
-      }
-      *reinterpret_cast<uint16_t*>(nan + t * 16 + ch * 2) = static_cast<uint16_t>(bits);
-      any |= bits;
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t nb = nan_bytes(*w[e]);
+      *w[e] &= ~nb;
+      bits |= ((nb & 1u) | (nb >> 7 & 2u) | (nb >> 14 & 4u) | (nb >> 21 & 8u)) << (4 * e);
     }
-    const bool sw = D == 128 && (ch & 4);
-    const uint32_t a0 = sw ? w[2] : w[0], a1 = sw ? w[3] : w[1], b0 = sw ? w[0] : w[2], b1 = sw ? w[1] : w[3];
-    const uint32_t row = dst + (ch >> 2) * kPanel + t * 128;
-    const int c0 = ((ch & 3) * 2 + (sw ? 1 : 0)) ^ (t & 7);
-    sts128(row + (c0 << 4), cvt_lo(a0), cvt_hi(a0), cvt_lo(a1), cvt_hi(a1));
-    sts128(row + ((c0 ^ 1) << 4), cvt_lo(b0), cvt_hi(b0), cvt_lo(b1), cvt_hi(b1));
+    *reinterpret_cast<uint16_t*>(nan + (t0 + i * kRowsPer) * 16 + ch * 2) = static_cast<uint16_t>(bits);
+    any |= bits;
   }
-  if (NANS) {
-    any = __any_sync(kFullMask, any != 0);
-    if (lane == 0) *nan_any = any;
-  }
+  any = __any_sync(kFullMask, any != 0);
+  if (lane == 0) *nan_any = any;
 }
 
 // tiles: tiles filled before the segment
 template <int D, int NM, bool U16>
 __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, uint8_t* smem, uint32_t tiles) {
-  using L = Lay<D, NM>;
+  using L = Lay<D, NM, U16>;
   constexpr int kAhead = NM == 1 ? 2 : 1;  // tiles whose codes are on the way
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 7, ch = lane % (D / 16);
-  const int64_t lane0 = (g.h * p.c.head16 + ch + (U16 ? lane / (D / 16) * p.c.token16 : 0)) * 16;
-  const uint8_t* kbase = p.c.k + lane0;
-  const uint8_t* vbase = p.c.v + lane0;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, ch = lane % (D / 16);
+  const bool is_v = threadIdx.x >> 7 & 1;
+  const uint8_t* base =
+      (is_v ? p.c.v : p.c.k) + (g.h * p.c.head16 + ch + (U16 ? lane / (D / 16) * p.c.token16 : 0)) * 16;
   const uint32_t row16 = static_cast<uint32_t>(p.c.token16);
-  const int end = min(g.x.n_keys, (g.u0 + g.n) * kKeys);
-  Translate tr(p, g.x, g.h, end);
-  const int e0 = g.u0 * kKeys + warp * 16 + (U16 ? 0 : lane & 15);
-  auto entry = [&](int j) { return e0 + j * kKeys; };
-  const int first_limit = p.sel_width ? INT32_MAX : row_limit(p, g.x, g.x.first);
-  Codes<D> c[kAhead];
-  auto take = [&](Codes<D>& d, const Translate::Scale& s) {
-    d.ks = s.ks, d.vs = s.vs, d.off = s.off16;
-    if (U16)
-      d.valid = s.pos == INT32_MAX ? 0 : min(end - s.pos, 16);
-    else
-      d.valid = __ballot_sync(kFullMask, s.pos != INT32_MAX);
+  // tokens from here on are not seen by all rows
+  const int partial = p.sel_width || !is_v ? INT32_MAX : row_limit(p, g.x, g.x.first) - g.u0 * kKeys;
+  const uint32_t dst = smem_u32(smem) + (is_v ? L::kV : L::kK);
+  uint64_t* empty = is_v ? bars->vempty : bars->kempty;
+  uint64_t* full = is_v ? bars->vfull : bars->kfull;
+  const int n = g.n;
+  uint4 c[kAhead][D / 16];
+  auto load = [&](int j, uint4(&r)[D / 16]) {
+    if (j >= n) return;
+    const uint32_t slot = (tiles + j) % L::kRing;
+    wait(bars, &bars->tfull[slot], (tiles + j) / L::kRing & 1);
+    load_codes<D, U16>(base, row16, reinterpret_cast<const uint2*>(smem + L::kPlace) + slot * L::kEntries, r);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->tempty[slot]);
   };
 #pragma unroll
-  for (int a = 0; a < kAhead; ++a) {
-    take(c[a], tr.scale(tr.page(tr.index(entry(a)))));
-    load_codes<D, U16>(kbase, row16, c[a].off, c[a].valid, c[a].k);
-    load_codes<D, U16>(vbase, row16, c[a].off, c[a].valid, c[a].v);
-  }
-  Translate::Page pg = tr.page(tr.index(entry(kAhead)));
-  Translate::Index ix = tr.index(entry(kAhead + 1));
-  for (int j0 = 0; j0 < g.n; j0 += kAhead) {
+  for (int a = 0; a < kAhead; ++a) load(a, c[a]);
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += kAhead) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int j = j0 + a;
-      if (j >= g.n) break;
-      Codes<D>& d = c[a];
-      const uint32_t t = tiles + j, slot = t & 1, parity = (t >> 1 & 1) ^ 1;
-      const Translate::Scale s = tr.scale(pg);
-      pg = tr.page(ix);
-      ix = tr.index(entry(j + kAhead + 2));
-      wait(bars, &bars->kempty[slot], parity);
-      store_codes<D, false>(smem_u32(smem) + L::kK + slot * L::kKV, d.k, nullptr, nullptr);
-      float* sc = reinterpret_cast<float*>(smem + L::kScale) + (t & (kScaleRing - 1)) * 384;
-      if (U16 ? lane == 0 : lane < 16) {
-        const int at = U16 ? warp : warp * 16 + lane;
-        const bool on = U16 ? d.valid > 0 : d.valid >> (lane & 15) & 1;
-        const float lvs = on ? __log2f(fmaxf(d.vs, kMinBlockScale)) : -INFINITY;
-        sc[at] = on ? d.ks : 0.f;
-        sc[128 + at] = lvs;
-        sc[256 + at] = on ? ex2(-lvs) : 0.f;
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->kfull[slot]);
-      const Codes<D> old = d;
-      take(d, s);
-      load_codes<D, U16>(kbase, row16, d.off, d.valid, d.k);
-      wait(bars, &bars->vempty[slot], parity);
+      if (j >= n) break;
+      const uint32_t t = tiles + j, slot = t & 1;
+      wait(bars, &empty[slot], (t >> 1 & 1) ^ 1);
       // Tokens that some rows see and others do not: a NaN among their values
       // must not reach the latter as 0 * NaN, so it is noted beside the tile.
-      const uint32_t vdst = smem_u32(smem) + L::kV + slot * L::kKV;
-      if ((g.u0 + j + 1) * kKeys > first_limit)
-        store_codes<D, true>(vdst, old.v, smem + L::kNan + slot * (128 * 16),
-                             reinterpret_cast<uint32_t*>(smem + L::kNanAny) + slot * 8 + warp);
-      else
-        store_codes<D, false>(vdst, old.v, nullptr, nullptr);
+      if ((j + 1) * kKeys > partial)
+        take_nans<D>(c[a], smem + L::kNan + slot * (128 * 16),
+                     reinterpret_cast<uint32_t*>(smem + L::kNanAny) + slot * 4 + warp);
+      store_codes<D>(dst + slot * L::kKV, c[a]);
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->vfull[slot]);
-      load_codes<D, U16>(vbase, row16, d.off, d.valid, d.v);
+      if (lane == 0) mbar_arrive(&full[slot]);
+      load(j + kAhead, c[a]);
     }
   }
 }
 
 // --------------------------------------------------------------- products --
 // One thread.  tiles: as above; phases: bit w, the parity of the tiles that stream w has had.
-template <int D, int NM>
+template <int D, int NM, bool U16>
 __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, uint32_t& phases,
                                          uint32_t segs) {
-  using L = Lay<D, NM>;
+  using L = Lay<D, NM, U16>;
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const uint32_t tm = bars->tmem, base = smem_u32(smem);
   constexpr uint32_t kScoreDesc = idesc_f16<128, kKeys, false>(), kValueDesc = idesc_f16<128, D, true>();
@@ -348,9 +384,9 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
 // ---------------------------------------------------------------- softmax --
 // Query rows to shared memory, scaled by a power of two (and the sign of the
 // score scale, so that a larger product is a larger score).
-template <int D, int NM>
+template <int D, int NM, bool U16>
 __device__ __forceinline__ void load_q(const AttendParams& p, const Segment& g, uint8_t* smem, bool f16) {
-  using L = Lay<D, NM>;
+  using L = Lay<D, NM, U16>;
   constexpr int kPer = D / 8, kPass = kSoftThreads / kPer;  // threads of a row, rows of a pass
   const int lane = threadIdx.x & 31, c = lane % kPer, sub = lane / kPer;
   const float sign = p.scale_log2 < 0.f ? -1.f : 1.f, mag = fabsf(p.scale_log2);
@@ -414,7 +450,7 @@ __device__ __forceinline__ float top_of(const uint32_t (&r)[32], int c, const fl
         const float s = __uint_as_float(r[q * 16 + e]);
         m = fmaxf(m, !MASKED || col + e < see ? s : -INFINITY);
       }
-      top = fmaxf(top, fmaf(m, sc[col / 16] * row.factor, sc[128 + col / 16]));
+      top = fmaxf(top, fmaf(m, sc[col / 16] * row.factor, sc[8 + col / 16]));
     } else {
 #pragma unroll
       for (int e = 0; e < 16; e += 4) {
@@ -442,7 +478,7 @@ __device__ __forceinline__ void weights_of(const uint32_t (&r)[32], int c, const
     const int col = c * 32 + q * 16;
     float2 sum = make_float2(0.f, 0.f);
     float kf = 0.f, c0 = 0.f;
-    if (U16) kf = sc[col / 16] * row.factor, c0 = sc[128 + col / 16] - ref;
+    if (U16) kf = sc[col / 16] * row.factor, c0 = sc[8 + col / 16] - ref;
 #pragma unroll
     for (int e = 0; e < 16; e += 4) {
       float4 ks, lv, iv;
@@ -468,7 +504,7 @@ __device__ __forceinline__ void weights_of(const uint32_t (&r)[32], int c, const
         out[q * 8 + (e + i) / 2] = half2_of(w.x, w.y);
       }
     }
-    row.l = U16 ? fmaf(sum.x + sum.y, sc[256 + col / 16], row.l) : row.l + (sum.x + sum.y);
+    row.l = U16 ? fmaf(sum.x + sum.y, sc[16 + col / 16], row.l) : row.l + (sum.x + sum.y);
   }
   tmem_st_x16(dst, out);
 }
@@ -554,11 +590,11 @@ __device__ __forceinline__ void store_out(const AttendParams& p, const Segment& 
 template <int D, int NM, bool U16>
 __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& seg, uint8_t* smem, uint32_t tiles,
                                         uint32_t& count, uint32_t segs, bool f16) {
-  using L = Lay<D, NM>;
+  using L = Lay<D, NM, U16>;
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int w = threadIdx.x >> 7, t = threadIdx.x & 127, lane = threadIdx.x & 31, first = t & ~31;
   static_assert(sizeof(Segment) <= 128, "");
-  load_q<D, NM>(p, seg, smem, f16);
+  load_q<D, NM, U16>(p, seg, smem, f16);
   // (the key loop has no registers for it)
   const Segment& g = *reinterpret_cast<Segment*>(smem + L::kSeg + (segs & 1) * 128);
   if (threadIdx.x == 0) *reinterpret_cast<Segment*>(smem + L::kSeg + (segs & 1) * 128) = seg;
@@ -586,7 +622,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
     ++count;
     tc_fence_after();
     if (busy) {
-      const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + ((tiles + j) & (kScaleRing - 1)) * 384;
+      const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (tiles + j) % L::kRing * (3 * L::kEntries);
       const int pos0 = (u0 + j) * kKeys;
       const bool fresh = j < kEvery;
       if (pos0 + kKeys > row.warp_limit) {
@@ -594,10 +630,10 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
         softmax_tile<D, U16, true>(tm_s, tm_o, sc, row, see, fresh);
         const uint32_t slot = (tiles + j) & 1;
         wait(bars, &bars->vfull[slot], (tiles + j) >> 1 & 1);
-        const uint32_t* any = reinterpret_cast<const uint32_t*>(smem + L::kNanAny) + slot * 8;
+        const uint32_t* any = reinterpret_cast<const uint32_t*>(smem + L::kNanAny) + slot * 4;
         uint32_t nans = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) nans |= any[e];
+        for (int e = 0; e < 4; ++e) nans |= any[e];
         if (nans) {
           const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + L::kNan) + slot * (128 * 4);
           for (int k = 0; k < see; ++k)
@@ -610,7 +646,10 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->pfull[w]);
+    if (lane == 0) {
+      mbar_arrive(&bars->pfull[w]);
+      mbar_arrive(&bars->tempty[(tiles + j) % L::kRing]);
+    }
   }
 
   wait(bars, &bars->ofull, segs & 1);
@@ -682,7 +721,7 @@ template <int D, int NM, bool U16>
 __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_constant__ AttendParams p, int f16) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  using L = Lay<D, NM>;
+  using L = Lay<D, NM, U16>;
   constexpr int R = NM * 128;
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   int* prefix = reinterpret_cast<int*>(smem + L::kPrefix);
@@ -691,14 +730,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   // The CTA's share of the units, or its one (tile, head): where it starts, and
   // its units.
   int tile, h, u0;
-  int64_t share;
+  int64_t share, start = 0, all = 0;
   if (p.n_ctas) {
     const int total = tile_prefix<kKeys, kThreads>(p, R, prefix, prefix + kMaxSplitTiles2 + 1);
     const int64_t units = static_cast<int64_t>(total) * p.c.heads, n = min(units, static_cast<int64_t>(p.n_ctas));
-    if (blockIdx.x >= n) return;
+    if (blockIdx.x >= n) {
+      if (threadIdx.x == 0) note_job(p, R, prefix, units, 0, 0);
+      return;
+    }
     const int64_t u = share_start(blockIdx.x, units, n), end = share_start(blockIdx.x + 1, units, n);
     const Piece c = piece_at(p, prefix, u, end);
     tile = c.tile, h = c.h, u0 = c.u0, share = end - u;
+    start = u, all = units;
   } else {
     tile = p.n_tiles - 1 - blockIdx.x / p.c.heads;  // those of a sequence that see most, first
     h = blockIdx.x % p.c.heads, u0 = 0;
@@ -711,12 +754,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   if (warp == 16) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&bars->kfull[i], kFillWarps);
-        mbar_init(&bars->vfull[i], kFillWarps);
+        mbar_init(&bars->kfull[i], kFillWarps / 2);
+        mbar_init(&bars->vfull[i], kFillWarps / 2);
         mbar_init(&bars->kempty[i], 1);
         mbar_init(&bars->vempty[i], 1);
         mbar_init(&bars->sfull[i], 1);
         mbar_init(&bars->pfull[i], 4);
+      }
+      for (int i = 0; i < L::kRing; ++i) {
+        mbar_init(&bars->tfull[i], 1);
+        mbar_init(&bars->tempty[i], kFillWarps + (NM == 2 ? 8 : 4));  // and the softmax warps that use the tile
       }
       mbar_init(&bars->qfull, kSoftThreads / 32);
       mbar_init(&bars->ofull, 1);
@@ -777,11 +824,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     return;
   }
   regs_to<Regs<NM>::kIssue>();
-  if (warp != 16) return;
+  if (warp != 16) {
+    each(true, [&](const Segment& g, uint32_t tiles, uint32_t) { look_up<D, NM, U16>(p, g, smem, tiles); });
+    if (warp == 17 && lane == 0 && p.n_ctas) note_job(p, R, prefix, all, start, start + share);
+    return;
+  }
   uint32_t gone = 1;
   if (lane == 0) {
     uint32_t phases = 0;
-    each(false, [&](const Segment& g, uint32_t tiles, uint32_t segs) { products<D, NM>(g.n, smem, tiles, phases, segs); });
+    each(false, [&](const Segment& g, uint32_t tiles, uint32_t segs) { products<D, NM, U16>(g.n, smem, tiles, phases, segs); });
     // All products have completed and all softmax warps have left before TMEM is
     // freed: these waits end by a time limit alone, and then it stays allocated.
     tc_commit(&bars->done);
@@ -796,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
 template <int D, int NM, bool U16>
 cudaError_t go_tile(const AttendParams& p, bool f16, int grid, cudaStream_t stream) {
   // (at least half of an SM's: one CTA an SM, since each takes all of its TMEM)
-  constexpr int kBytes = Lay<D, NM>::kBytes > 118784 ? Lay<D, NM>::kBytes : 118784;
+  constexpr int kBytes = Lay<D, NM, U16>::kBytes > 118784 ? Lay<D, NM, U16>::kBytes : 118784;
   static_assert(kBytes <= 232448, "");
   // The shares of registers presume those of the launch: with fewer, the waits for
   // more would not end.

@@ -77,7 +77,7 @@ struct AttendPlan {
   bool f16;
   int D, rows;   // rows of a tile: up to 16, the streaming kernel
   int grid;
-  size_t off_prefix, off_ml, off_o, bytes;
+  size_t off_jobs, off_ml, off_o, bytes;
 };
 
 indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, const indexer_attention* a,
@@ -124,8 +124,8 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   p.n_ctas = split ? slots : 0;
   pl->grid = split ? slots : static_cast<int>(items);
   size_t at = 0;
-  pl->off_prefix = at;
-  at += split ? align256((tiles + 1) * sizeof(int32_t)) : 0;
+  pl->off_jobs = at;
+  at += split ? align256(static_cast<size_t>(slots) * sizeof(JoinJob)) : 0;
   pl->off_ml = at;
   at += split ? align256(static_cast<size_t>(2) * slots * R * sizeof(float2)) : 0;
   pl->off_o = at;
@@ -236,7 +236,7 @@ indexer_status indexer_cache_attend(const indexer_cache* cache, const indexer_se
   p.sel_len = sel_len;
   p.status = reinterpret_cast<uint32_t*>(status);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.prefix = reinterpret_cast<int32_t*>(ws + pl.off_prefix);
+  p.jobs = reinterpret_cast<JoinJob*>(ws + pl.off_jobs);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   p.part_o = reinterpret_cast<float*>(ws + pl.off_o);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
