@@ -37,7 +37,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kLaunchRegs = 96;
 template <int NM>
 struct Regs {
-  static constexpr int kSoft = NM == 2 ? 144 : 112, kFill = NM == 2 ? 72 : 104, kIssue = 48;
+  static constexpr int kSoft = 128, kFill = 88, kIssue = 48;
   static_assert(kSoftThreads * kSoft + kFillWarps * 32 * kFill + 128 * kIssue <= kThreads * kLaunchRegs, "");
 };
 
@@ -63,20 +63,22 @@ template <int D, int NM, bool U16>
 struct Lay {
   static constexpr int kPanels = D / 64;
   static constexpr int kEntries = U16 ? 8 : 128;  // look-ups of a tile
+  static constexpr int kScales = U16 ? 32 : 384;  // their floats: a float4 each, or an array of each
   static constexpr int kRing = U16 || NM == 1 ? 8 : 4;  // tiles whose look-ups are kept
   static constexpr int kKV = kPanels * kPanel;   // a K or V tile
-  static constexpr int kQ = 0;                   // [NM][kPanels] panels; the exchange of NM = 1
+  static constexpr int kQ = 0;                   // [NM][kPanels] panels; then the outputs' stage
   static constexpr int kK = kQ + NM * kKV;       // [2]
   static constexpr int kV = kK + 2 * kKV;        // [2]
-  static constexpr int kScale = kV + 2 * kKV;    // [kRing][3][entries]: key scale, log2 value scale, 1 / value scale
-  static constexpr int kPlace = kScale + kRing * 3 * kEntries * 4;  // [kRing][entries]: place and number
+  static constexpr int kScale = kV + 2 * kKV;    // [kRing][kScales]: key scales, log2 value scales, 1 / value scales
+  static constexpr int kPlace = kScale + kRing * kScales * 4;  // [kRing][entries]: place and number
   static constexpr int kNan = kPlace + kRing * kEntries * 8;  // [2][128][4]: NaN codes of V tokens, a bit a dimension
   static constexpr int kNanAny = kNan + 2 * 128 * 16;             // [2][4]: a word a value warp, not 0 where it has any
   static constexpr int kRowNan = kNanAny + 64;                    // [256][4]: dimensions made NaN, by row
   static constexpr int kFactor = kRowNan + 256 * 16;              // [256]
   static constexpr int kMl = kFactor + 1024;                      // [128] float2
   static constexpr int kSeg = kMl + 1024;                         // [2] the softmax warps' Segment
-  static constexpr int kBars = kSeg + 256;
+  static constexpr int kEx = kSeg + 256;                          // NM = 1: [128] rows of 32 columns
+  static constexpr int kBars = kEx + (NM == 1 ? 128 * 128 : 0);
   static constexpr int kPrefix = kBars + 320;                     // [kMaxSplitTiles2 + 1] and 17 sums
   static constexpr int kBytes = kPrefix + (kMaxSplitTiles2 + 1) * 4 + 128 + 1024;
 };
@@ -89,8 +91,18 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
                : "l"(p));
   return v;
 }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -103,12 +115,24 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w &
 
 // A wait that, once it has run out, makes every further wait of the CTA end at
 // once: the loops then run through on whatever the buffers hold, all within
-// bounds, and the rows become NaN.  (A try suspends the thread for about a
-// microsecond, so the limit is some seconds.)
-constexpr int kWaitTries = 1 << 21;
+// bounds, and the rows become NaN.  A try suspends the thread for up to
+// kTryNs, so that waiting warps take no issue slots from the others.
+constexpr uint32_t kTryNs = 100000;
+constexpr int kWaitTries = 100000;
+__device__ __forceinline__ bool try_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(kTryNs)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void wait(Bars* b, uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; !mbar_try_wait(bar, parity); ++i)
+  for (int i = 0; !try_long(bar, parity); ++i)
     if (i >= kWaitTries || *reinterpret_cast<volatile int*>(&b->abort)) {
       *reinterpret_cast<volatile int*>(&b->abort) = 1;
       return;
@@ -162,14 +186,18 @@ __device__ __forceinline__ void look_up(const AttendParams& p, const Segment& g,
     if (on_lane) wait(bars, &bars->tempty[slot], parity);
     __syncwarp();
     if (on_lane) {
-      float* sc = reinterpret_cast<float*>(smem + L::kScale) + slot * (3 * kEntries);
+      float* sc = reinterpret_cast<float*>(smem + L::kScale) + slot * L::kScales;
       uint2* place = reinterpret_cast<uint2*>(smem + L::kPlace) + slot * kEntries;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
         const int k = e * 32 + en;
         const bool on = at[e].pos != INT32_MAX;
         const float lvs = on ? __log2f(fmaxf(vs[e], kMinBlockScale)) : -INFINITY;
-        sc[k] = ks[e], sc[kEntries + k] = lvs, sc[2 * kEntries + k] = on ? ex2(-lvs) : 0.f;
+        const float ivs = on ? ex2(-lvs) : 0.f;
+        if (U16)
+          reinterpret_cast<float4*>(sc)[k] = make_float4(ks[e], lvs, ivs, 0.f);
+        else
+          sc[k] = ks[e], sc[kEntries + k] = lvs, sc[2 * kEntries + k] = ivs;
         place[k] = make_uint2(at[e].off16, on ? (U16 ? min(end - at[e].pos, 16) : 1) : 0);
       }
     }
@@ -251,7 +279,7 @@ __device__ __forceinline__ void take_nans(uint4 (&r)[D / 16], uint8_t* nan, uint
 template <int D, int NM, bool U16>
 __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, uint8_t* smem, uint32_t tiles) {
   using L = Lay<D, NM, U16>;
-  constexpr int kAhead = NM == 1 ? 2 : 1;  // tiles whose codes are on the way
+  constexpr int kAhead = 1;  // tiles whose codes are on the way
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, ch = lane % (D / 16);
   const bool is_v = threadIdx.x >> 7 & 1;
@@ -345,12 +373,10 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
     tc_commit(&bars->kempty[tiles & 1]);
     for (int i = 0; i < n; ++i) {
       vready(i);
+      if (i + 1 < n) kready(i + 1);
       pready(0);
       value(0, i, i == 0);
-      if (i + 1 < n) {
-        kready(i + 1);
-        score(0, i + 1);
-      }
+      if (i + 1 < n) score(0, i + 1);
       pready(1);
       value(1, i, i == 0);
       tc_commit(&bars->vempty[(tiles + i) & 1]);
@@ -368,11 +394,11 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
     for (int i = 0; i < n; ++i) {
       const int w = i & 1;
       vready(i);
+      if (i + 2 < n) kready(i + 2);
       pready(w);
       value(w, i, i < 2);
       tc_commit(&bars->vempty[(tiles + i) & 1]);
       if (i + 2 < n) {
-        kready(i + 2);
         score(w, i + 2);
         tc_commit(&bars->kempty[(tiles + i) & 1]);
       }
@@ -382,208 +408,255 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
 }
 
 // ---------------------------------------------------------------- softmax --
-// Query rows to shared memory, scaled by a power of two (and the sign of the
-// score scale, so that a larger product is a larger score).
+// Query rows to shared memory as FP16, scaled by a power of two (and the sign of
+// the score scale, so that a larger product is a larger score): copied as they
+// are, then each row converted in place by a thread.
 template <int D, int NM, bool U16>
 __device__ __forceinline__ void load_q(const AttendParams& p, const Segment& g, uint8_t* smem, bool f16) {
   using L = Lay<D, NM, U16>;
-  constexpr int kPer = D / 8, kPass = kSoftThreads / kPer;  // threads of a row, rows of a pass
-  const int lane = threadIdx.x & 31, c = lane % kPer, sub = lane / kPer;
-  const float sign = p.scale_log2 < 0.f ? -1.f : 1.f, mag = fabsf(p.scale_log2);
-  constexpr int kU = 4;
-  for (int rw = (threadIdx.x >> 5) * (32 / kPer); rw < g.x.rows; rw += kU * kPass) {
-    const int r0 = rw + sub;
-    uint4 raw[kU];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int r = r0 + u * kPass, pair = g.x.first + r;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (r < g.x.rows)
-        raw[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (g.x.q0 + pair / p.G) * p.q_stride +
-                                                      (g.h * p.G + pair % p.G) * (2 * D)) + c);
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int r = r0 + u * kPass;
-      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-      float2 f[4];
-      float m = 0.f;
+  constexpr int kPer = D / 8, kPass = kSoftThreads / kPer;  // 16-byte chunks of a row, rows of a pass
+  const int c = threadIdx.x % kPer;
+  const uint32_t q = smem_u32(smem) + L::kQ;
+  auto place = [&](int r, int ch) {
+    return q + (r >> 7) * L::kKV + (ch >> 3) * kPanel + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+  };
+#pragma unroll 4
+  for (int r = threadIdx.x / kPer; r < g.x.rows; r += kPass) {
+    const int pair = g.x.first + r, query = pair / p.G;
+    cp_async16(place(r, c), p.q + (g.x.q0 + query) * p.q_stride + (g.h * p.G + pair - query * p.G) * (2 * D) + c * 16,
+               true);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  named_bar(kSoftBar, kSoftThreads);
+  const int r = threadIdx.x;
+  if (r >= g.x.rows) return;
+  float s = 1.f;
+  if (!f16) {
+    float m = 0.f;
+#pragma unroll 4
+    for (int ch = 0; ch < kPer; ++ch) {
+      const uint4 v = lds128(place(r, ch));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        f[e] = f16 ? unpack_act<true>(w[e]) : unpack_act<false>(w[e]);
-        m = fmaxf(m, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
+        const float2 f = unpack_act<false>(w[e]);
+        m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
       }
-#pragma unroll
-      for (int o = kPer / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-      const float s = f16 ? 1.f : row_pow2(m), inv = sign / s;
-      if (r >= g.x.rows) continue;
-      sts128(smem_u32(smem) + L::kQ + (r >> 7) * L::kKV + (c >> 3) * kPanel + (r & 127) * 128 +
-                 (((c & 7) ^ (r & 7)) << 4),
-             half2_of(f[0].x * inv, f[0].y * inv), half2_of(f[1].x * inv, f[1].y * inv),
-             half2_of(f[2].x * inv, f[2].y * inv), half2_of(f[3].x * inv, f[3].y * inv));
-      if (c == 0) reinterpret_cast<float*>(smem + L::kFactor)[r] = s * mag;
     }
+    s = row_pow2(m);
+  }
+  const float inv = (p.scale_log2 < 0.f ? -1.f : 1.f) / s;
+  reinterpret_cast<float*>(smem + L::kFactor)[r] = s * fabsf(p.scale_log2);
+  if (f16 && inv > 0.f) return;
+#pragma unroll 4
+  for (int ch = 0; ch < kPer; ++ch) {
+    const uint32_t a = place(r, ch);
+    const uint4 v = lds128(a);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = f16 ? unpack_act<true>(w[e]) : unpack_act<false>(w[e]);
+      w[e] = half2_of(f.x * inv, f.y * inv);
+    }
+    sts128(a, w[0], w[1], w[2], w[3]);
   }
 }
 
 struct Row {
   float m, l;      // reference, and the sum
   float factor;
-  int limit;       // positions that the row sees
-  int warp_limit;  // the least of its warp's
 };
 
-// Scales of 16 columns from `at` on.
-__device__ __forceinline__ float4 lds_f4(const float* s, int at) { return *reinterpret_cast<const float4*>(s + at); }
+// The scales of 16 columns: one entry of each (U16), or sixteen.
+template <bool U16>
+struct Scales {
+  const float* s;  // of the tile
+  int col;
+  __device__ __forceinline__ float4 all() const { return *reinterpret_cast<const float4*>(s + col / 4); }  // U16
+  __device__ __forceinline__ float4 four(int which, int e) const {
+    return *reinterpret_cast<const float4*>(s + which * 128 + col + e);
+  }
+};
 
-// Largest score, in base 2 and with the value's scale, of 32 columns.
+// Largest score, in base 2 and with the value's scale, of 16 columns; those from `see` on are not seen.
 template <bool U16, bool MASKED>
-__device__ __forceinline__ float top_of(const uint32_t (&r)[32], int c, const float* sc, const Row& row, int see,
-                                        float top) {
+__device__ __forceinline__ float top_of(const uint32_t* r, const Scales<U16>& sc, const Row& row, int see) {
+  float top = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int col = c * 32 + q * 16;
-    if (U16) {
-      float m = -INFINITY;
+  for (int e = 0; e < 16; e += 4) {
+    float4 ks, lv;
+    if (!U16) ks = sc.four(0, e), lv = sc.four(1, e);
+    const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {lv.x, lv.y, lv.z, lv.w};
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float s = __uint_as_float(r[q * 16 + e]);
-        m = fmaxf(m, !MASKED || col + e < see ? s : -INFINITY);
+    for (int i = 0; i < 4; i += 2) {
+      float u[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        u[k] = __uint_as_float(r[e + i + k]);
+        if (!U16) u[k] = fmaf(u[k], k4[i + k] * row.factor, v4[i + k]);
+        if (MASKED && sc.col + e + i + k >= see) u[k] = -INFINITY;
       }
-      top = fmaxf(top, fmaf(m, sc[col / 16] * row.factor, sc[8 + col / 16]));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const float4 ks = lds_f4(sc, col + e), lv = lds_f4(sc + 128, col + e);
-        const float k4[4] = {ks.x, ks.y, ks.z, ks.w}, v4[4] = {lv.x, lv.y, lv.z, lv.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = fmaf(__uint_as_float(r[q * 16 + e + i]), k4[i] * row.factor, v4[i]);
-          top = fmaxf(top, !MASKED || col + e + i < see ? u : -INFINITY);
-        }
-      }
+      top = max3(top, u[0], u[1]);
     }
+  }
+  if (U16) {
+    const float4 a = sc.all();
+    top = fmaf(top, a.x * row.factor, a.y);
   }
   return top;
 }
 
-// Weights of 32 columns to TMEM, and their share of the row's sum.
+// Weights of 16 columns, two a word, and their share of the row's sum.
 template <bool U16, bool MASKED>
-__device__ __forceinline__ void weights_of(const uint32_t (&r)[32], int c, const float* sc, Row& row, int see,
-                                           uint32_t dst) {
+__device__ __forceinline__ void weights_of(const uint32_t (&r)[16], const Scales<U16>& sc, const Row& row, int see,
+                                           float& l, uint32_t* out) {
   const float ref = row.m == -INFINITY ? 0.f : row.m - kHead;
-  uint32_t out[16];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int col = c * 32 + q * 16;
-    float2 sum = make_float2(0.f, 0.f);
-    float kf = 0.f, c0 = 0.f;
-    if (U16) kf = sc[col / 16] * row.factor, c0 = sc[8 + col / 16] - ref;
-#pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-      float4 ks, lv, iv;
-      if (!U16) ks = lds_f4(sc, col + e), lv = lds_f4(sc + 128, col + e), iv = lds_f4(sc + 256, col + e);
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const float2 s = make_float2(__uint_as_float(r[q * 16 + e + i]), __uint_as_float(r[q * 16 + e + i + 1]));
-        float2 k2 = make_float2(kf, kf), c2 = make_float2(c0, c0);
-        if (!U16) {
-          k2 = mul2(i ? make_float2(ks.z, ks.w) : make_float2(ks.x, ks.y), make_float2(row.factor, row.factor));
-          c2 = add2(i ? make_float2(lv.z, lv.w) : make_float2(lv.x, lv.y), make_float2(-ref, -ref));
-        }
-        const float2 u = fma2(s, k2, c2);
-        float2 w = make_float2(ex2(u.x), ex2(u.y));
-        if (MASKED) {
-          if (col + e + i >= see) w.x = 0.f;
-          if (col + e + i + 1 >= see) w.y = 0.f;
-        }
-        if (U16)
-          sum = add2(sum, w);
-        else
-          sum = fma2(w, i ? make_float2(iv.z, iv.w) : make_float2(iv.x, iv.y), sum);
-        out[q * 8 + (e + i) / 2] = half2_of(w.x, w.y);
-      }
-    }
-    row.l = U16 ? fmaf(sum.x + sum.y, sc[16 + col / 16], row.l) : row.l + (sum.x + sum.y);
+  float2 sum = make_float2(0.f, 0.f), kf, c0;
+  float4 a;
+  if (U16) {
+    a = sc.all();
+    kf = make_float2(a.x * row.factor, a.x * row.factor), c0 = make_float2(a.y - ref, a.y - ref);
   }
-  tmem_st_x16(dst, out);
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) {
+    float4 ks, lv, iv;
+    if (!U16) ks = sc.four(0, e), lv = sc.four(1, e), iv = sc.four(2, e);
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      if (!U16) {
+        kf = mul2(i ? make_float2(ks.z, ks.w) : make_float2(ks.x, ks.y), make_float2(row.factor, row.factor));
+        c0 = add2(i ? make_float2(lv.z, lv.w) : make_float2(lv.x, lv.y), make_float2(-ref, -ref));
+      }
+      const float2 u = fma2(make_float2(__uint_as_float(r[e + i]), __uint_as_float(r[e + i + 1])), kf, c0);
+      float2 w = make_float2(ex2(u.x), ex2(u.y));
+      if (MASKED) {
+        if (sc.col + e + i >= see) w.x = 0.f;
+        if (sc.col + e + i + 1 >= see) w.y = 0.f;
+      }
+      sum = U16 ? add2(sum, w) : fma2(w, i ? make_float2(iv.z, iv.w) : make_float2(iv.x, iv.y), sum);
+      out[(e + i) / 2] = half2_of(w.x, w.y);
+    }
+  }
+  l = U16 ? fmaf(sum.x + sum.y, a.z, l) : l + (sum.x + sum.y);
 }
 
-// One tile of a stream: its weights, and the rise of its rows' references.
-// tm_s, tm_o: the warp's lanes of the stream's scores and outputs; fresh: no
-// output yet.
+// One tile of a stream: the rise of its rows' references, and its weights.  see:
+// tokens that the row sees (MASKED; otherwise all).  tm_s, tm_o: the warp's
+// lanes of the stream's scores and outputs; fresh: no output yet.  Two passes
+// over the scores in TMEM, in loops that are not unrolled further: all roles'
+// hot code together has to stay in the instruction cache (with one long pass,
+// or both unrolled, every role waited for its own code).
 template <int D, bool U16, bool MASKED>
 __device__ __forceinline__ void softmax_tile(uint32_t tm_s, uint32_t tm_o, const float* sc, Row& row, int see,
                                              bool fresh) {
-  // The loops are not unrolled further: all roles' code together has to stay in
-  // the instruction cache (unrolled, the issuing warp waited for its own code).
-  uint32_t a[32], b[32];
   float top = -INFINITY;
 #pragma unroll 1
-  for (int c = 0; c < 4; c += 2) {
-    tmem_ld_x32(tm_s + c * 32, a);
-    tmem_ld_x32(tm_s + c * 32 + 32, b);
+  for (int c = 0; c < 128; c += 64) {
+    uint32_t a[32], b[32];
+    tmem_ld_x32(tm_s + c, a);
+    tmem_ld_x32(tm_s + c + 32, b);
     tmem_wait_ld(a);
     tmem_wait_ld(b);
-    top = top_of<U16, MASKED>(a, c, sc, row, see, top);
-    top = top_of<U16, MASKED>(b, c + 1, sc, row, see, top);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      top = fmaxf(top, top_of<U16, MASKED>((q < 2 ? a : b) + (q & 1) * 16, Scales<U16>{sc, c + q * 16}, row, see));
   }
+  uint32_t a[16], b[16], w[8];
+  tmem_ld_x16(tm_s, a);
   if (__any_sync(kFullMask, top > row.m + kSlack)) {
     const float m = fmaxf(row.m, top), f = m == row.m ? 1.f : ex2(row.m - m);
     row.m = m;
     row.l *= f;
     if (!fresh) {
 #pragma unroll 1
-      for (int i = 0; i < D / 16; ++i) {  // (rare)
-        uint32_t o[16];
-        tmem_ld_x16(tm_o + i * 16, o);
-        tmem_wait_ld(o);
+      for (int c = 0; c < D; c += 16) {
+        tmem_ld_x16(tm_o + c, b);
+        tmem_wait_ld(b);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-        tmem_st_x16(tm_o + i * 16, o);
+        for (int e = 0; e < 16; ++e) b[e] = __float_as_uint(__uint_as_float(b[e]) * f);
+        tmem_st_x16(tm_o + c, b);
       }
     }
   }
   // A piece's weights take the place of half its scores, and of no later ones.
-  tmem_ld_x32(tm_s, a);
+  constexpr int kBody = MASKED ? 32 : 64;
 #pragma unroll 1
-  for (int c = 0; c < 4; c += 2) {
-    tmem_wait_ld(a);
-    tmem_ld_x32(tm_s + c * 32 + 32, b);
-    weights_of<U16, MASKED>(a, c, sc, row, see, tm_s + c * 16);
-    tmem_wait_ld(b);
-    if (c == 0) tmem_ld_x32(tm_s + 64, a);
-    weights_of<U16, MASKED>(b, c + 1, sc, row, see, tm_s + c * 16 + 16);
+  for (int c0 = 0; c0 < 128; c0 += kBody) {
+#pragma unroll
+    for (int c = 0; c < kBody; c += 32) {
+      const int col = c0 + c;
+      tmem_wait_ld(a);
+      tmem_ld_x16(tm_s + col + 16, b);
+      weights_of<U16, MASKED>(a, Scales<U16>{sc, col}, row, see, row.l, w);
+      tmem_st_x8(tm_s + col / 2, w);
+      tmem_wait_ld(b);
+      if (col + 32 < 128) tmem_ld_x16(tm_s + col + 32, a);
+      weights_of<U16, MASKED>(b, Scales<U16>{sc, col + 16}, row, see, row.l, w);
+      tmem_st_x8(tm_s + col / 2 + 8, w);
+    }
   }
   tmem_wait_st();
 }
 
-// 32 output columns of a row.
-__device__ __forceinline__ void store_out(const AttendParams& p, const Segment& g, int D, int rows, int i, int col,
-                                          const float (&o)[32], const Row& row, uint32_t nan, bool f16) {
-  const bool none = row.m == -INFINITY;
-  if (g.whole) {
-    const int pair = g.x.first + i;
-    const int64_t at = (g.x.q0 + pair / p.G) * static_cast<int64_t>(p.Hq) + g.h * p.G + pair % p.G;
-    const float inv = none ? 0.f : 1.f / row.l;
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float lo = nan >> (2 * e) & 1 ? NAN : o[2 * e] * inv, hi = nan >> (2 * e + 1) & 1 ? NAN : o[2 * e + 1] * inv;
-      w[e] = f16 ? pack_act<true>(lo, hi) : pack_act<false>(lo, hi);
-    }
-    uint4* dst = reinterpret_cast<uint4*>(p.out + (at * D + col) * 2);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-    if (p.lse && col == 0) p.lse[at] = none ? -INFINITY : kLn2 * (row.m - kHead + log2f(row.l));
+// A warp's 32 rows, i0 the first: whole ones as outputs, others as parts.  get(c,
+// o): columns 32c .. of the lane's row (all lanes take part).  The rows go
+// through `stage`, 2 D bytes each, so that they are written in full lines.
+template <int D, class Get>
+__device__ __forceinline__ void write_rows(const AttendParams& p, const Segment& g, uint32_t stage, int R, int i0,
+                                           const Row& row, const uint32_t* nan, bool f16, Get&& get) {
+  const int lane = threadIdx.x & 31, i = i0 + lane, count = min(g.x.rows - i0, 32);
+  const bool none = row.m == -INFINITY, whole = g.whole;
+  int at = 0;  // the row's place among the outputs, or the parts
+  if (whole) {
+    const int pair = g.x.first + i, query = pair / p.G;
+    at = (g.x.q0 + query) * p.Hq + g.h * p.G + pair - query * p.G;
+    if (p.lse && lane < count) p.lse[at] = none ? -INFINITY : kLn2 * (row.m - kHead + log2f(row.l));
   } else {
-    float4* dst = reinterpret_cast<float4*>(p.part_o + (g.part * rows + i) * D + col);
-    float v[32];
+    at = static_cast<int>(g.part) * R + i;
+    if (lane < count) p.part_ml[at] = make_float2(row.m, row.l);
+  }
+  const float mul = !whole ? 1.f : none ? 0.f : 1.f / row.l;
+  constexpr int kChunks = D / 8;  // 16-byte chunks of a row of the stage
+  const uint32_t mine = stage + lane * (2 * D), sw = lane & 7;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    float o[32];
+    get(c, o);
+    const uint32_t bits = nan[c];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = nan >> e & 1 ? NAN : o[e];
+    for (int e = 0; e < 32; ++e) o[e] = bits >> e & 1 ? NAN : o[e] * mul;
+    if (whole) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-    if (col == 0) p.part_ml[g.part * rows + i] = make_float2(row.m, row.l);
+      for (int e = 0; e < 4; ++e) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = f16 ? pack_act<true>(o[8 * e + 2 * k], o[8 * e + 2 * k + 1])
+                     : pack_act<false>(o[8 * e + 2 * k], o[8 * e + 2 * k + 1]);
+        sts128(mine + (((c * 4 + e) ^ sw) << 4), w[0], w[1], w[2], w[3]);
+      }
+      if (c + 1 < D / 32) continue;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        sts128(mine + (((c * 8 + e) % kChunks ^ sw) << 4), __float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+               __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+      if ((c + 1) * 8 % kChunks) continue;
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int k = lane; k < 32 * kChunks; k += 32) {
+      const int r = k / kChunks, ch = k % kChunks;
+      const int to = __shfl_sync(kFullMask, at, r);
+      if (r < count) {
+        const uint4 v = lds128(stage + r * (2 * D) + ((ch ^ (r & 7)) << 4));
+        uint8_t* dst = whole ? p.out + static_cast<int64_t>(to) * (2 * D)
+                             : reinterpret_cast<uint8_t*>(p.part_o + static_cast<int64_t>(to) * D + (c + 1) * 32 - D / 2);
+        *reinterpret_cast<uint4*>(dst + ch * 16) = v;
+      }
+    }
+    __syncwarp();
   }
 }
 
@@ -611,23 +684,26 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
   Row row;
   row.m = -INFINITY, row.l = 0.f;
   row.factor = reinterpret_cast<const float*>(smem + L::kFactor)[i];
-  row.limit = p.sel_width ? INT32_MAX : row_limit(p, g.x, g.x.first + i);
-  row.warp_limit = p.sel_width ? INT32_MAX : row_limit(p, g.x, g.x.first + min(r0 + first, g.x.rows - 1));
+  // Tiles of the segment that all of the warp's rows see whole.
+  const int whole_tiles =
+      p.sel_width ? g.n : (row_limit(p, g.x, g.x.first + min(r0 + first, g.x.rows - 1)) - g.u0 * kKeys) / kKeys;
   const uint32_t lanes = static_cast<uint32_t>(first) << 16, tm = bars->tmem + lanes;
   const uint32_t tm_s = tm + w * 128, tm_o = tm + 256 + w * 128;
   constexpr int kEvery = NM == 2 ? 1 : 2;
-  const int n = g.n, u0 = g.u0;
+  const int n = g.n;
   for (int j = NM == 2 ? 0 : w; j < n; j += kEvery) {
     wait(bars, &bars->sfull[w], count & 1);
     ++count;
     tc_fence_after();
     if (busy) {
-      const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (tiles + j) % L::kRing * (3 * L::kEntries);
-      const int pos0 = (u0 + j) * kKeys;
-      const bool fresh = j < kEvery;
-      if (pos0 + kKeys > row.warp_limit) {
-        const int see = max(min(row.limit - pos0, kKeys), 0);
-        softmax_tile<D, U16, true>(tm_s, tm_o, sc, row, see, fresh);
+      const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (tiles + j) % L::kRing * L::kScales;
+      const bool partial = j >= whole_tiles;
+      if (!partial) {
+        softmax_tile<D, U16, false>(tm_s, tm_o, sc, row, kKeys, j < kEvery);
+      } else {
+        const int see =
+            min(row_limit(p, g.x, g.x.first + min(r0 + t, g.x.rows - 1)) - (g.u0 + j) * kKeys, kKeys);
+        softmax_tile<D, U16, true>(tm_s, tm_o, sc, row, see, j < kEvery);
         const uint32_t slot = (tiles + j) & 1;
         wait(bars, &bars->vfull[slot], (tiles + j) >> 1 & 1);
         const uint32_t* any = reinterpret_cast<const uint32_t*>(smem + L::kNanAny) + slot * 4;
@@ -640,8 +716,6 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) row_nan[e] |= bits[k * 4 + e];
         }
-      } else {
-        softmax_tile<D, U16, false>(tm_s, tm_o, sc, row, kKeys, fresh);
       }
     }
     tc_fence_before();
@@ -656,64 +730,60 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
   tc_fence_after();
   if (*reinterpret_cast<volatile int*>(&bars->abort)) row.l = NAN;
   if (isnan(row.l)) row.m = 0.f;  // a row of NaN scores counts in a join
-  constexpr int kRows = NM * 128;
+  const uint32_t stage = smem_u32(smem) + L::kQ + (threadIdx.x >> 5) * (64 * D);  // (all products are done)
   if (NM == 2) {
-    if (busy) {
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+    if (busy)
+      write_rows<D>(p, g, stage, 256, r0 + first, row, row_nan, f16, [&](int c, float (&o)[32]) {
         uint32_t r[32];
         tmem_ld_x32(tm_o + c * 32, r);
         tmem_wait_ld(r);
-        float o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]);
-        if (r0 + t < g.x.rows) store_out(p, g, D, kRows, r0 + t, c * 32, o, row, row_nan[c], f16);
-      }
-    }
+      });
+    named_bar(kSoftBar, kSoftThreads);  // (a stage may be where another warp's next queries go)
     return;
   }
-  // NM = 1: the second stream hands its rows over, 32 columns at a time, in the
-  // queries' place (the products that read them are done).
+  // NM = 1: the second stream hands its rows over, 32 columns at a time.
   float2* ml = reinterpret_cast<float2*>(smem + L::kMl);
-  uint8_t* ex = smem + L::kQ + t * 128;
+  const uint32_t ex = smem_u32(smem) + L::kEx + t * 128;
   if (w == 1) ml[t] = make_float2(row.m, row.l);
-  const uint32_t* other_nan = row_nan + 128 * 4;
-  float f0 = 1.f, f1 = 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
-    uint32_t r[32];
-    if (busy) {
+  named_bar(kSoftBar, kSoftThreads);
+  if (w == 1) {
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t r[32];
       tmem_ld_x32(tm_o + c * 32, r);
       tmem_wait_ld(r);
-    }
-    if (w == 1 && busy) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        *reinterpret_cast<uint4*>(ex + ((e ^ (t & 7)) << 4)) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+      for (int e = 0; e < 8; ++e) sts128(ex + ((e ^ (t & 7)) << 4), r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+      named_bar(kSoftBar, kSoftThreads);
+      named_bar(kSoftBar, kSoftThreads);
     }
-    named_bar(kSoftBar, kSoftThreads);
-    if (w == 0 && busy) {
-      if (c == 0) {
-        const float2 o = ml[t];
-        const float m = fmaxf(row.m, o.x);
-        f0 = row.m == -INFINITY ? 0.f : ex2(row.m - m);
-        f1 = o.x == -INFINITY ? 0.f : ex2(o.x - m);
-        row.l = (f0 == 0.f ? 0.f : f0 * row.l) + (f1 == 0.f ? 0.f : f1 * o.y);
-        row.m = m;
-      }
-      float o[32];
+  } else {
+    const float2 other = ml[t];
+    const float m = fmaxf(row.m, other.x);
+    const float f0 = row.m == -INFINITY ? 0.f : ex2(row.m - m), f1 = other.x == -INFINITY ? 0.f : ex2(other.x - m);
+    row.l = (f0 == 0.f ? 0.f : f0 * row.l) + (f1 == 0.f ? 0.f : f1 * other.y);
+    row.m = m;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) row_nan[e] |= row_nan[128 * 4 + e];
+    write_rows<D>(p, g, stage, 128, first, row, row_nan, f16, [&](int c, float (&o)[32]) {
+      uint32_t r[32];
+      tmem_ld_x32(tm_o + c * 32, r);
+      tmem_wait_ld(r);
+      named_bar(kSoftBar, kSoftThreads);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float4 v = *reinterpret_cast<const float4*>(ex + ((e ^ (t & 7)) << 4));
-        const float b[4] = {v.x, v.y, v.z, v.w};
+        const uint4 v = lds128(ex + ((e ^ (t & 7)) << 4));
+        const uint32_t b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[4 * e + k] = (f0 == 0.f ? 0.f : f0 * __uint_as_float(r[4 * e + k])) + (f1 == 0.f ? 0.f : f1 * b[k]);
+          o[4 * e + k] = (f0 == 0.f ? 0.f : f0 * __uint_as_float(r[4 * e + k])) + (f1 == 0.f ? 0.f : f1 * __uint_as_float(b[k]));
       }
-      if (t < g.x.rows) store_out(p, g, D, kRows, t, c * 32, o, row, row_nan[c] | other_nan[c], f16);
-    }
-    named_bar(kSoftBar, kSoftThreads);
+      named_bar(kSoftBar, kSoftThreads);
+    });
   }
+  named_bar(kSoftBar, kSoftThreads);
 }
 
 // ----------------------------------------------------------------- kernel --
