@@ -326,10 +326,11 @@ __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, ui
 }
 
 // --------------------------------------------------------------- products --
-// One thread.  tiles: as above; phases: bit w, the parity of the tiles that stream w has had.
+// One warp.  tiles: as above; phases: bit w, the parity of the tiles that stream
+// w has had; one: true for the lane that issues.
 template <int D, int NM, bool U16>
-__device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, uint32_t& phases,
-                                         uint32_t segs) {
+__device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, uint32_t& phases, uint32_t segs,
+                                         uint32_t one) {
   using L = Lay<D, NM, U16>;
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const uint32_t tm = bars->tmem, base = smem_u32(smem);
@@ -345,16 +346,16 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
 #pragma unroll 1
     for (int s = 0; s < D / 16; ++s) {
       const uint32_t at = ((s >> 2) * kPanel + (s & 3) * 32) >> 4;
-      tc_mma_f16(tm + w * 128, desc(q + at), desc(k + at), kScoreDesc, s > 0);
+      tc_mma_f16_one(one, tm + w * 128, desc(q + at), desc(k + at), kScoreDesc, s > 0);
     }
-    tc_commit(&bars->sfull[w]);
+    tc_commit_one(one, &bars->sfull[w]);
   };
   auto value = [&](int w, int i, bool first) {
     uint32_t v = v0 + ((tiles + i) & 1) * (L::kKV >> 4);
     asm volatile("" : "+r"(v));
 #pragma unroll 1
     for (int s = 0; s < kKeys / 16; ++s)
-      tc_mma_f16_ts(tm + 256 + w * 128, tm + w * 128 + s * 8, desc(v + s * (2048 >> 4)), kValueDesc,
+      tc_mma_f16_ts_one(one, tm + 256 + w * 128, tm + w * 128 + s * 8, desc(v + s * (2048 >> 4)), kValueDesc,
                     !(first && s == 0));
   };
   auto kready = [&](int i) { wait(bars, &bars->kfull[(tiles + i) & 1], (tiles + i) >> 1 & 1); };
@@ -370,7 +371,7 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
     kready(0);
     score(0, 0);
     score(1, 0);
-    tc_commit(&bars->kempty[tiles & 1]);
+    tc_commit_one(one, &bars->kempty[tiles & 1]);
     for (int i = 0; i < n; ++i) {
       vready(i);
       if (i + 1 < n) kready(i + 1);
@@ -379,17 +380,17 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
       if (i + 1 < n) score(0, i + 1);
       pready(1);
       value(1, i, i == 0);
-      tc_commit(&bars->vempty[(tiles + i) & 1]);
+      tc_commit_one(one, &bars->vempty[(tiles + i) & 1]);
       if (i + 1 < n) {
         score(1, i + 1);
-        tc_commit(&bars->kempty[(tiles + i + 1) & 1]);
+        tc_commit_one(one, &bars->kempty[(tiles + i + 1) & 1]);
       }
     }
   } else {
     for (int i = 0; i < min(n, 2); ++i) {
       kready(i);
       score(i, i);
-      tc_commit(&bars->kempty[(tiles + i) & 1]);
+      tc_commit_one(one, &bars->kempty[(tiles + i) & 1]);
     }
     for (int i = 0; i < n; ++i) {
       const int w = i & 1;
@@ -397,14 +398,14 @@ __device__ __forceinline__ void products(int n, uint8_t* smem, uint32_t tiles, u
       if (i + 2 < n) kready(i + 2);
       pready(w);
       value(w, i, i < 2);
-      tc_commit(&bars->vempty[(tiles + i) & 1]);
+      tc_commit_one(one, &bars->vempty[(tiles + i) & 1]);
       if (i + 2 < n) {
         score(w, i + 2);
-        tc_commit(&bars->kempty[(tiles + i) & 1]);
+        tc_commit_one(one, &bars->kempty[(tiles + i) & 1]);
       }
     }
   }
-  tc_commit(&bars->ofull);
+  tc_commit_one(one, &bars->ofull);
 }
 
 // ---------------------------------------------------------------- softmax --
@@ -564,8 +565,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t tm_s, uint32_t tm_o, const
   }
   uint32_t a[16], b[16], w[8];
   tmem_ld_x16(tm_s, a);
-  if (__any_sync(kFullMask, top > row.m + kSlack)) {
-    const float m = fmaxf(row.m, top), f = m == row.m ? 1.f : ex2(row.m - m);
+  const bool up = top > row.m + kSlack;  // (a row's own affair: its results do not depend on its neighbours)
+  if (__any_sync(kFullMask, up)) {
+    const float m = up ? top : row.m, f = up ? ex2(row.m - m) : 1.f;
     row.m = m;
     row.l *= f;
     if (!fresh) {
@@ -899,19 +901,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
     if (warp == 17 && lane == 0 && p.n_ctas) note_job(p, R, prefix, all, start, start + share);
     return;
   }
-  uint32_t gone = 1;
-  if (lane == 0) {
-    uint32_t phases = 0;
-    each(false, [&](const Segment& g, uint32_t tiles, uint32_t segs) { products<D, NM, U16>(g.n, smem, tiles, phases, segs); });
-    // All products have completed and all softmax warps have left before TMEM is
-    // freed: these waits end by a time limit alone, and then it stays allocated.
-    tc_commit(&bars->done);
-    gone = mbar_wait(&bars->done, 0u, nullptr, kWaitLimitNs) && mbar_wait(&bars->left, 0u, nullptr, kWaitLimitNs);
-    if (p.status && (bars->abort || !gone)) atomicOr(p.status, kStatusWaitTimeout);
-  }
-  gone = __shfl_sync(kFullMask, gone, 0);
+  const uint32_t one = elect_lane();
+  uint32_t phases = 0;
+  each(false, [&](const Segment& g, uint32_t tiles, uint32_t segs) {
+    products<D, NM, U16>(g.n, smem, tiles, phases, segs, one);
+  });
+  // All products have completed and all softmax warps have left before TMEM is
+  // freed: these waits end by a time limit alone, and then it stays allocated.
+  tc_commit_one(one, &bars->done);
+  const bool gone = mbar_wait(&bars->done, 0u, nullptr, kWaitLimitNs) && mbar_wait(&bars->left, 0u, nullptr, kWaitLimitNs);
+  const bool all_gone = __all_sync(kFullMask, gone);
+  if (p.status && one && (bars->abort || !all_gone)) atomicOr(p.status, kStatusWaitTimeout);
   tc_fence_after();
-  if (gone) tmem_dealloc(bars->tmem, kTmemCols);
+  if (all_gone) tmem_dealloc(bars->tmem, kTmemCols);
 }
 
 template <int D, int NM, bool U16>
