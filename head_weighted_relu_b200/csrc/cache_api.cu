@@ -89,7 +89,8 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   st = view_seqs(s, pointers, &p.s);
   if (st != INDEXER_OK) return st;
   if (!a || !act_ok(a->act) || a->Hq < 1 || a->Hq % c->heads != 0 || a->sel_width < 0 || a->max_q < 0 ||
-      (a->causal != 0 && a->causal != 1) || !isfinite(a->scale))
+      (a->causal != 0 && a->causal != 1) || !isfinite(a->scale) || a->kernel < INDEXER_ATTEND_AUTO ||
+      a->kernel > INDEXER_ATTEND_TILE)
     return INDEXER_EINVAL;
   p.Hq = a->Hq;
   p.G = a->Hq / c->heads;
@@ -108,7 +109,16 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   // rows that share a pass over the keys: of a query with a selection, of a
   // sequence without
   const int64_t most_rows = a->sel_width ? p.G : static_cast<int64_t>(a->max_q ? a->max_q : s->S) * p.G;
-  const int R = pl->rows = most_rows <= 8 ? 8 : most_rows <= 16 ? 16 : most_rows <= 128 ? 128 : 256;
+  const int64_t most_keys = a->sel_width ? a->sel_width : p.max_keys;
+  // Streaming costs about 0.9 us for every 128 keys and head that a CTA goes
+  // over, for every 16 rows; tiles 1.7 us (128 rows) whatever the rows, and some
+  // 20 us more a launch: 9 x 5 queries of 8 heads over 6K tokens take 35 and 41
+  // us, one query of 64 heads over 1M tokens 258 and 115 us.
+  const double units = static_cast<double>(a->sel_width ? s->S : s->B) * c->heads * most_keys / 128 / sms;
+  const int64_t passes = (most_rows + 15) / 16;
+  const bool tile = a->kernel == INDEXER_ATTEND_TILE ||
+                    (a->kernel == INDEXER_ATTEND_AUTO && passes > 2 && units * (0.9 * passes - 1.7) > 30);
+  const int R = pl->rows = tile ? (most_rows <= 128 ? 128 : 256) : (most_rows <= 8 ? 8 : 16);
   p.sel_tiles = (p.G + R - 1) / R;
   const int64_t tiles = a->sel_width ? s->S * p.sel_tiles : s->S * p.G / R + s->B;
   const int64_t items = tiles * c->heads;
@@ -118,7 +128,6 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   const int slots = stream ? sms * attend_stream_ctas_per_sm(R) : sms;
   // Fewer (tile, head)s than fill the SMs a few times over: the CTAs share all
   // keys equally, across tiles, and a second kernel joins the parts.
-  const int64_t most_keys = a->sel_width ? a->sel_width : p.max_keys;
   const bool split = tiles <= (stream ? kMaxSplitTiles : kMaxSplitTiles2) && items < 8 * slots &&
                      tiles * (most_keys / 64 + 1) <= INT32_MAX;
   p.n_ctas = split ? slots : 0;

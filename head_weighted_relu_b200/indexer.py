@@ -64,6 +64,7 @@ class Problem(ctypes.Structure):
 
 
 ACT_BF16, ACT_FP16 = 0, 1
+ATTEND_AUTO, ATTEND_STREAM, ATTEND_TILE = 0, 1, 2   # kernels of cache_attend
 STATUS_TOKEN = 8   # status bit of the cache calls: a token's page or position does not exist
 
 
@@ -91,7 +92,8 @@ class Sequences(ctypes.Structure):
 class Attention(ctypes.Structure):
     """Mirror of indexer_attention."""
     _fields_ = [("Hq", ctypes.c_int32), ("act", ctypes.c_int32), ("causal", ctypes.c_int32),
-                ("sel_width", ctypes.c_int32), ("max_q", ctypes.c_int32), ("scale", ctypes.c_float)]
+                ("sel_width", ctypes.c_int32), ("max_q", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("kernel", ctypes.c_int32)]
 
 
 def _load():
@@ -636,7 +638,7 @@ def cache_append(cache: KVCache, k, v, cu_q, kv_len, page_table, table=None, int
 
 
 def cache_attend(cache: KVCache, q, cu_q, kv_len, page_table, scale=None, causal=True, selected=None, max_q=0,
-                 with_lse=False, out=None, workspace=None, status=None, stream=None):
+                 with_lse=False, out=None, workspace=None, status=None, stream=None, kernel=ATTEND_AUTO):
     """Attention of q [S, Hq, D] (bf16 or fp16, already rotated) over the cache:
     out [S, Hq, D], and with_lse=True also the log-sum-exp [S, Hq] float32.
 
@@ -646,9 +648,9 @@ def cache_attend(cache: KVCache, q, cu_q, kv_len, page_table, scale=None, causal
     returns them for positions counted from the sequence's start, narrows that to
     the positions named.  A row that sees nothing gives 0 and -inf.  scale
     defaults to D ** -0.5.  max_q: rows of the longest sequence, if known (it
-    chooses the kernel: results may differ by roundings).  workspace: a uint8
-    tensor kept by the caller (its size from `cache_attend_workspace_bytes`); by
-    default it is allocated for the call.
+    chooses the kernel: results may differ by roundings; or name it by `kernel`).
+    workspace: a uint8 tensor kept by the caller (its size from
+    `cache_attend_workspace_bytes`); by default it is allocated for the call.
     """
     device = _device_of(cache.k)
     desc = cache.descriptor()
@@ -665,7 +667,8 @@ def cache_attend(cache: KVCache, q, cu_q, kv_len, page_table, scale=None, causal
         if width < 1:
             raise ValueError("selected indices must be [S, W] with W > 0")
         si, sl = _ints(idx, "selected indices", device, (S, width)), _ints(lens, "selected lengths", device, (S,))
-    att = Attention(Hq, act, 1 if causal else 0, width, max_q, scale if scale is not None else 1 / math.sqrt(desc.D))
+    att = Attention(Hq, act, 1 if causal else 0, width, max_q, scale if scale is not None else 1 / math.sqrt(desc.D),
+                    kernel)
     if workspace is None:
         workspace = _new(stream, device, (_attend_workspace(device, desc, seqs, att),), torch.uint8)
     elif workspace.get_device() != device or not workspace.is_contiguous():
@@ -694,9 +697,10 @@ def _attend_workspace(device, desc, seqs, att) -> int:
     return n.value
 
 
-def cache_attend_workspace_bytes(cache: KVCache, q, cu_q, kv_len, page_table, selected_width=0, max_q=0) -> int:
+def cache_attend_workspace_bytes(cache: KVCache, q, cu_q, kv_len, page_table, selected_width=0, max_q=0,
+                                 kernel=ATTEND_AUTO) -> int:
     """Bytes of workspace for `cache_attend` on these tensors' shapes."""
     device = _device_of(cache.k)
     desc = cache.descriptor()
     return _attend_workspace(device, desc, _sequences(q.shape[0], cu_q, kv_len, page_table, device),
-                             Attention(q.shape[1], _act(q, "q"), 1, selected_width, max_q, 1.0))
+                             Attention(q.shape[1], _act(q, "q"), 1, selected_width, max_q, 1.0, kernel))

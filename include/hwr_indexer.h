@@ -482,7 +482,18 @@ typedef struct {
   int32_t max_q;      /* rows of the longest sequence, or 0 if unknown: it
                          chooses the kernel, and so may change roundings */
   float scale;        /* finite */
+  int32_t kernel;     /* indexer_attend_kernel: a given one does not depend on the
+                         batch, and a row's result in it only on how its keys are
+                         divided */
 } indexer_attention;
+
+/* Kernels of indexer_cache_attend: up to 16 query rows (queries times heads
+ * per key/value head) share a pass over the keys, or up to 256. */
+typedef enum {
+  INDEXER_ATTEND_AUTO = 0,
+  INDEXER_ATTEND_STREAM = 1,
+  INDEXER_ATTEND_TILE = 2
+} indexer_attend_kernel;
 
 /* Workspace of indexer_cache_attend: scratch between calls, no
  * initialisation; calls that may overlap on the GPU need one each. */

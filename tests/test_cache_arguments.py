@@ -37,7 +37,7 @@ def _append(I, cache=None, seqs=None, k=PTR, v=PTR, stride=1024, act=0, rot=None
 
 
 def _attend(I, cache=None, seqs=None, att=None, q=PTR, stride=8192, si=None, sl=None, out=PTR, ws=PTR, n=1 << 40):
-    a = dict(Hq=64, act=0, causal=1, sel_width=0, max_q=0, scale=0.1)
+    a = dict(Hq=64, act=0, causal=1, sel_width=0, max_q=0, scale=0.1, kernel=0)
     a.update(att or {})
     return I._lib.indexer_cache_attend(cache or _cache(I), seqs or _seqs(I),
                                        I.Attention(*[a[f] for f, _ in I.Attention._fields_]), q, stride, si, sl, out,
@@ -96,7 +96,8 @@ def test_append_arguments(I):
 def test_attend_arguments(I):
     for att, status in ((dict(Hq=60), EINVAL), (dict(Hq=0), EINVAL), (dict(Hq=8 * 129), EUNSUPPORTED), (dict(act=7), EINVAL),
                         (dict(causal=2), EINVAL), (dict(sel_width=-1), EINVAL), (dict(scale=float("nan")), EINVAL),
-                        (dict(scale=float("inf")), EINVAL), (dict(max_q=-1), EINVAL)):
+                        (dict(scale=float("inf")), EINVAL), (dict(max_q=-1), EINVAL), (dict(kernel=3), EINVAL),
+                        (dict(kernel=-1), EINVAL)):
         assert _attend(I, att=att) == status, att
     assert _attend(I, seqs=_seqs(I, table_pages=1 << 28, table_stride=1 << 28)) == EUNSUPPORTED
 

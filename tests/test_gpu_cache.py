@@ -320,11 +320,20 @@ ATTENDS = [
     ([90], [100], 33, 1, 128, 64, 64, "bf16", False, True),
     ([260], [700], 16, 4, 128, 64, 64, "fp16", True, False),
     ([1] * 40, list(range(1, 401, 10)), 64, 8, 128, 16, 16, "bf16", True, False),
+    ([1, 3], [5000, 3001], 64, 1, 128, 64, 32, "bf16", True, False),
+    ([40, 1], [2500, 1700], 16, 2, 64, 24, 8, "fp16", True, False),     # a scale every 8 tokens, many tiles
+    ([150], [2900], 6, 2, 128, 48, 4, "bf16", True, False),
+    ([70], [3100], 8, 2, 128, 128, 64, "fp16", True, True),
+    ([1], [1], 64, 1, 64, 16, 16, "bf16", True, False),
 ]
 
 
+STREAM, TILE = 1, 2   # the kernels, as the binding numbers them
+
+
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
 @pytest.mark.parametrize("case", ATTENDS, ids=lambda c: f"q{str(c[0])[:12]}-H{c[2]}.{c[3]}-D{c[4]}-{c[7]}-{'c' if c[8] else 'n'}")
-def test_cache_attend(cuda_ok, case):
+def test_cache_attend(cuda_ok, case, kernel):
     I = _I()
     q_lens, kv_len, Hq, heads, D, page, block, act, causal, hnd = case
     rng = np.random.default_rng(len(q_lens) * 1000 + Hq + D)
@@ -336,11 +345,12 @@ def test_cache_attend(cuda_ok, case):
     out = torch.full((S, Hq, D), 7.0, dtype=ACT[act], device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     args = (cache, q, _dev(cu), _dev(np.array(kv_len, dtype=np.int32)), _dev(table))
-    got, lse = I.cache_attend(*args, causal=causal, with_lse=True, out=out, status=status, max_q=max(q_lens))
+    kw = dict(causal=causal, with_lse=True, max_q=max(q_lens), kernel=kernel)
+    got, lse = I.cache_attend(*args, out=out, status=status, **kw)
     assert status.item() == 0
     owned = _check_attend(cache, q, cu, kv_len, table, D ** -0.5, causal, None, got, lse, act)
     assert (out[int(cu[-1]):] == 7.0).all() and owned.sum() == cu[-1]
-    again, lse2 = I.cache_attend(*args, causal=causal, with_lse=True, max_q=max(q_lens))
+    again, lse2 = I.cache_attend(*args, **kw)
     n = int(cu[-1])
     assert torch.equal(got[:n], again[:n]) and torch.equal(lse[:n], lse2[:n])      # the same sums in the same order
 
@@ -356,8 +366,9 @@ SELECTED = [
 ]
 
 
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
 @pytest.mark.parametrize("case", SELECTED, ids=lambda c: f"q{c[0]}-H{c[2]}.{c[3]}-D{c[4]}-W{c[8]}")
-def test_cache_attend_selected(cuda_ok, case):
+def test_cache_attend_selected(cuda_ok, case, kernel):
     I = _I()
     q_lens, kv_len, Hq, heads, D, page, block, act, W = case
     rng = np.random.default_rng(W)
@@ -378,11 +389,12 @@ def test_cache_attend_selected(cuda_ok, case):
         ln[r] = n
     sel = (_dev(idx), _dev(ln))
     out, lse = I.cache_attend(cache, q, _dev(cu), _dev(np.array(kv_len, dtype=np.int32)), _dev(table),
-                              scale=0.11, selected=sel, with_lse=True)
+                              scale=0.11, selected=sel, with_lse=True, kernel=kernel)
     _check_attend(cache, q, cu, kv_len, table, 0.11, True, sel, out, lse, act)
 
 
-def test_attend_extreme_scores_and_scales(cuda_ok):
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+def test_attend_extreme_scores_and_scales(cuda_ok, kernel):
     """Scores of hundreds, value scales that differ by 2^60 within a sequence, and
     queries near the ends of their type's range."""
     I = _I()
@@ -391,12 +403,39 @@ def test_attend_extreme_scores_and_scales(cuda_ok):
     cache.v_scale[torch.from_numpy(table[0, :3].astype(np.int64)).cuda()] *= 2.0 ** -60
     q = _dev(rng.normal(size=(4, 8, 128)) * np.array([1e-30, 1e-3, 30.0, 300.0])[:, None, None], torch.bfloat16)
     cu, kv = np.array([0, 4], dtype=np.int32), [500]
-    out, lse = I.cache_attend(cache, q, _dev(cu), _dev(np.array(kv, dtype=np.int32)), _dev(table), with_lse=True)
+    out, lse = I.cache_attend(cache, q, _dev(cu), _dev(np.array(kv, dtype=np.int32)), _dev(table), with_lse=True, kernel=kernel)
     _check_attend(cache, q, cu, kv, table, 128 ** -0.5, True, None, out, lse, "bf16")
 
 
-@pytest.mark.parametrize("G", [4, 40])
-def test_attend_nan_reaches_only_rows_that_see_it(cuda_ok, G):
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+def test_attend_references_that_keep_rising(cuda_ok, kernel):
+    """Keys sorted so that later ones score higher by hundreds, in steps of every
+    size: the running references rise again and again, within a tile too."""
+    I = _I()
+    rng = np.random.default_rng(14)
+    kv, D = [900], 128
+    cache, table = _filled(rng, kv, 1, D, 64, 16)
+    q = _dev(np.ones((3, 40, D)) * np.linspace(-1, 1, 40)[None, :, None], torch.bfloat16)
+    for p in range(900):   # every dimension alike: the score is their value
+        pg, o = table[0, p // 64], p % 64
+        v = 448.0 * (p / 900) ** 2
+        cache.k[pg, o, 0] = int(R.to_code(np.array(v)))
+        cache.k_scale[pg, o // 16, 0] = 2.0 ** -5
+    cu = np.array([0, 3], dtype=np.int32)
+    out, lse = I.cache_attend(cache, q, _dev(cu), _dev(np.array(kv, dtype=np.int32)), _dev(table), with_lse=True, scale=0.1,
+                              kernel=kernel)
+    _check_attend(cache, q, cu, kv, table, 0.1, True, None, out, lse, "bf16")
+    # the other sign of the scale turns the scores round
+    out, lse = I.cache_attend(cache, q, _dev(cu), _dev(np.array(kv, dtype=np.int32)), _dev(table), with_lse=True, scale=-0.1,
+                              kernel=kernel)
+    _check_attend(cache, q, cu, kv, table, -0.1, True, None, out, lse, "bf16")
+    out, lse = I.cache_attend(cache, q, _dev(cu), _dev(np.array(kv, dtype=np.int32)), _dev(table), with_lse=True, scale=0.0,
+                              kernel=kernel)
+    _check_attend(cache, q, cu, kv, table, 0.0, True, None, out, lse, "bf16")
+
+
+@pytest.mark.parametrize("G,kernel", [(4, STREAM), (40, STREAM), (4, TILE), (40, TILE)])
+def test_attend_nan_reaches_only_rows_that_see_it(cuda_ok, G, kernel):
     """A NaN among the newest token's keys or values, or in one query: the rows
     before it stay as they are without it."""
     I = _I()
@@ -405,26 +444,28 @@ def test_attend_nan_reaches_only_rows_that_see_it(cuda_ok, G):
     cu, kv = np.array([0, 4], dtype=np.int32), [70]
     q = _dev(rng.normal(size=(4, 2 * G, 64)), torch.float16)
     args = (_dev(cu), _dev(np.array(kv, dtype=np.int32)), _dev(table))
-    clean = I.cache_attend(cache, q, *args)
+    clean = I.cache_attend(cache, q, *args, kernel=kernel)
     pg, o = table[0, 69 // 32], 69 % 32
     cache.v[pg, o, 1, 7] = 0x7F
-    got = I.cache_attend(cache, q, *args)
+    got = I.cache_attend(cache, q, *args, kernel=kernel)
     assert torch.equal(got[:3], clean[:3]) and torch.equal(got[3, :G], clean[3, :G])
     assert got[3, G:, 7].isnan().all() and torch.equal(got[3, G:, :7], clean[3, G:, :7])
     cache.v[pg, o, 1, 7] = 0
     cache.k[pg, o, 0, 3] = 0xFF
-    got = I.cache_attend(cache, q, *args)
+    got = I.cache_attend(cache, q, *args, kernel=kernel)
     assert torch.equal(got[:3], I.cache_attend(cache, q[:3].contiguous(), _dev(np.array([0, 3], dtype=np.int32)),
-                                               _dev(np.array([69], dtype=np.int32)), args[2]))
+                                               _dev(np.array([69], dtype=np.int32)), args[2],
+                                               kernel=kernel))
     assert got[3, :G].isnan().all() and not got[3, G:].isnan().any()
     cache.k[pg, o, 0, 3] = 0
     q2 = q.clone()
     q2[1, 0, 0] = float("nan")
-    got = I.cache_attend(cache, q2, *args)
+    got = I.cache_attend(cache, q2, *args, kernel=kernel)
     assert got[1, 0].isnan().all() and not got[1, 1:].isnan().any() and not got[[0, 2, 3]].isnan().any()
 
 
-def test_attend_passes_over_bad_pages(cuda_ok):
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+def test_attend_passes_over_bad_pages(cuda_ok, kernel):
     I = _I()
     rng = np.random.default_rng(6)
     cache, table = _filled(rng, [100, 50, 64], 2, 64, 16, 16)
@@ -436,7 +477,7 @@ def test_attend_passes_over_bad_pages(cuda_ok):
     cu = np.array([0, 2, 3, 4], dtype=np.int32)
     q = _dev(rng.normal(size=(4, 4, 64)), torch.bfloat16)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out, lse = I.cache_attend(cache, q, _dev(cu), kv_dev, _dev(t2), with_lse=True, status=status)
+    out, lse = I.cache_attend(cache, q, _dev(cu), kv_dev, _dev(t2), with_lse=True, status=status, kernel=kernel)
     assert status.item() == I.STATUS_TOKEN
     _check_attend(cache, q, cu, kv, t2, 64 ** -0.5, True, None, out, lse, "bf16")
     assert (out[2] == 0).all()
@@ -456,7 +497,8 @@ def test_attend_shares_pages_between_sequences(cuda_ok):
 
 # ---------------------------------------------------------- streams, graphs --
 
-def test_attend_on_another_stream_and_in_graphs(cuda_ok):
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+def test_attend_on_another_stream_and_in_graphs(cuda_ok, kernel):
     """A side stream, and two captured graphs that share one workspace, replayed
     with new lengths and pages in the same buffers."""
     I = _I()
@@ -466,24 +508,24 @@ def test_attend_on_another_stream_and_in_graphs(cuda_ok):
     kv = _dev(np.array([900, 300], dtype=np.int32))
     tb = _dev(table)
     q = _dev(rng.normal(size=(2, 16, 128)), torch.bfloat16)
-    want = I.cache_attend(cache, q, cu, kv, tb)
+    want = I.cache_attend(cache, q, cu, kv, tb, kernel=kernel)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    got = I.cache_attend(cache, q, cu, kv, tb, stream=side)
+    got = I.cache_attend(cache, q, cu, kv, tb, stream=side, kernel=kernel)
     side.synchronize()
     assert torch.equal(got, want)
-    ws = torch.empty(I.cache_attend_workspace_bytes(cache, q, cu, kv, tb), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(I.cache_attend_workspace_bytes(cache, q, cu, kv, tb, kernel=kernel), dtype=torch.uint8, device="cuda")
     outs, graphs = [], []
     for _ in range(2):
         out = torch.zeros_like(want)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            I.cache_attend(cache, q, cu, kv, tb, out=out, workspace=ws)
+            I.cache_attend(cache, q, cu, kv, tb, out=out, workspace=ws, kernel=kernel)
         outs.append(out)
         graphs.append(g)
     for lens in ([900, 300], [850, 299], [1, 64]):
         kv.copy_(_dev(np.array(lens, dtype=np.int32)))
-        want = I.cache_attend(cache, q, cu, kv, tb)
+        want = I.cache_attend(cache, q, cu, kv, tb, kernel=kernel)
         ws.fill_(0xFF)
         for g, out in zip(graphs, outs):
             out.zero_()
