@@ -126,6 +126,7 @@ struct AppendParams {
   uint32_t* status;
   int32_t kv_slots, kv_split;  // grid layout, set by the launcher
   int32_t q_slots, q_heads;
+  int32_t q_apart;             // q is a kernel of its own
 };
 cudaError_t launch_cache_append(AppendParams p, int D, bool f16, int sms, cudaStream_t stream);
 

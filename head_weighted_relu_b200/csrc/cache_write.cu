@@ -142,21 +142,25 @@ __global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __r
 #pragma unroll
       for (int o = kLanes<D> / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFullMask, m, o));
       if (!ok || !(m < INFINITY)) m = NAN;  // the whole row becomes NaN codes
-      const float sc = m == 0.f ? 1.f : __fdiv_rn(m, 448.f), inv = __fdividef(1.f, sc);
-      // code = RNE_e4m3(y / sc).  z = y * inv is within 8 units in the last place
-      // of the quotient, which decides the code unless a border between two codes
-      // is that near: for |z| >= 2^-6 a number of 5 significant bits, the last of
-      // them set (bit 19 of its pattern).  There, and below 2^-6, the quotient
-      // itself is taken: about 2% of warp steps of normal values.
-      float z[8], least = INFINITY;
-      uint32_t gap = 0xFFFFFFFFu;
+      // scale = m / 448 and code = RNE_e4m3(y / scale), both quotients rounded to
+      // nearest by a residual step (Markstein, 1990): with r the correctly rounded
+      // reciprocal of b and q = a r, the quotient is q + r (a - q b), unless b's
+      // fraction is all ones or something leaves the normal range.  Such rows
+      // take the division itself.
+      constexpr float k448 = 1.f / 448.f;
+      const float q0 = m * k448;
+      float sc = fmaf(fmaf(-q0, 448.f, m), k448, q0);
+      const bool plain = sc > 0x1p-60f && sc < 0x1p60f && (__float_as_uint(sc) & 0x7FFFFFu) != 0x7FFFFFu;
+      float z[8];
+      if (__all_sync(kFullMask, plain)) {
+        const float inv = __frcp_rn(sc);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        z[i] = y[i] * inv;
-        least = fminf(least, fabsf(z[i]));
-        gap = min(gap, (__float_as_uint(z[i]) + (8u - 0x80000u)) & 0xFFFFFu);
-      }
-      if (gap <= 16u || !(least >= 0x1p-6f) || !(inv < 0x1p126f)) {
+        for (int i = 0; i < 8; ++i) {
+          const float q = y[i] * inv;
+          z[i] = fmaf(fmaf(-q, sc, y[i]), inv, q);
+        }
+      } else {
+        sc = m == 0.f ? 1.f : __fdiv_rn(m, 448.f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = __fdiv_rn(y[i], sc);
       }
@@ -182,48 +186,64 @@ __device__ __forceinline__ float block_scale(float amax) {
 
 // Keys and values.  CTAs [0, kv_slots * kv_split): slot = one block of tokens
 // (floor(rows/block) + 2 slots a sequence), split over the 2*heads key and
-// value heads.  A (block, head) is taken by a team of warps, 4 warp steps of
-// rows each, whose 16-bit values stay in registers between the maximum and the
-// quantisation: every row is read once, and rotated twice.  Then q: 16 warps x
-// 256/D rows x a share of the query heads per CTA.
-constexpr int kAppendWarps = 16;
-constexpr int kSteps = 4;
+// value heads.  A (block, head) is taken by a team of warps, 4 or 8 warp steps of
+// rows each, whose rotated values stay in registers between the maximum and the
+// quantisation: every row is read once.  Then q, or in a
+// kernel of its own: 8 warps x 256/D rows x a share of the query heads per CTA.
+constexpr int kAppendWarps = 8;
+constexpr int kAppendCtas = 2;  // of an SM
 
+// Rotates the rows r of q and its share of the heads; i: the CTA's number among those for q.
+template <int D, bool F16, int U>
+__device__ __forceinline__ void rotate_q(const AppendParams& p, int i) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes<D>, rsub = lane / kLanes<D>;
+  const int r = (i % p.q_slots * kAppendWarps + warp) * kRows<D> + rsub;
+  const int h0 = i / p.q_slots * p.q_heads, h1 = min(p.Hq, h0 + p.q_heads);
+  Angles a;
+  bool ok = r < p.s.S && r < seq_row(p.s, p.s.B);
+  if (ok) {
+    const int b = slot_owner(p.s, r, 1, 1, 0);
+    const int pos = __ldg(p.s.kv_len + b) - (seq_row(p.s, b + 1) - r);
+    ok = pos >= 0 && (p.r.rot == 0 || pos < p.r.rows);
+    if (ok && p.r.rot) load_angles(p.r, pos, sub, a);
+    if (!ok && sub == 0 && h0 == 0 && p.status) atomicOr(p.status, kStatusToken);
+  }
+  const uint8_t* in = p.q + r * p.q_stride + sub * 16;
+  uint8_t* out = p.q_out + (static_cast<int64_t>(r) * p.Hq) * (2 * D) + sub * 16;
+  for (int h = h0; h < h1; h += U) {
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      raw[u] = ok && h + u < h1 ? __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * (2 * D)))
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float y[8];
+      rotate<D, F16>(p.r, raw[u], sub, a, y);
+      const uint4 o = make_uint4(pack_act<F16>(y[0], y[1]), pack_act<F16>(y[2], y[3]), pack_act<F16>(y[4], y[5]),
+                                 pack_act<F16>(y[6], y[7]));
+      if (ok && h + u < h1) *reinterpret_cast<uint4*>(out + (h + u) * (2 * D)) = o;
+    }
+  }
+}
+
+// q of many rows, beside the kernel for keys and values: with its registers (two
+// CTAs an SM) the copy would wait for memory.
 template <int D, bool F16>
-__global__ void __launch_bounds__(kAppendWarps * 32, 1) cache_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 5) cache_q_kernel(const __grid_constant__ AppendParams p) {
+  rotate_q<D, F16, 2>(p, blockIdx.x);
+  // complete no earlier than the kernel that this one did not wait for
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// kSteps: warp steps of rows that a warp holds
+template <int D, bool F16, int kSteps>
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) cache_append_kernel(const __grid_constant__ AppendParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes<D>, rsub = lane / kLanes<D>;
   const int kv_ctas = p.kv_slots * p.kv_split;
+  if (p.q_apart) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (static_cast<int>(blockIdx.x) >= kv_ctas) {
-    const int i = blockIdx.x - kv_ctas;
-    const int r = (i % p.q_slots * kAppendWarps + warp) * kRows<D> + rsub;
-    const int h0 = i / p.q_slots * p.q_heads, h1 = min(p.Hq, h0 + p.q_heads);
-    Angles a;
-    bool ok = r < p.s.S && r < seq_row(p.s, p.s.B);
-    if (ok) {
-      const int b = slot_owner(p.s, r, 1, 1, 0);
-      const int pos = __ldg(p.s.kv_len + b) - (seq_row(p.s, b + 1) - r);
-      ok = pos >= 0 && (p.r.rot == 0 || pos < p.r.rows);
-      if (ok && p.r.rot) load_angles(p.r, pos, sub, a);
-      if (!ok && sub == 0 && h0 == 0 && p.status) atomicOr(p.status, kStatusToken);
-    }
-    const uint8_t* in = p.q + r * p.q_stride + sub * 16;
-    uint8_t* out = p.q_out + (static_cast<int64_t>(r) * p.Hq) * (2 * D) + sub * 16;
-    constexpr int U = 8;
-    for (int h = h0; h < h1; h += U) {
-      uint4 raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        raw[u] = ok && h + u < h1 ? __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * (2 * D)))
-                                  : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float y[8];
-        rotate<D, F16>(p.r, raw[u], sub, a, y);
-        const uint4 o = make_uint4(pack_act<F16>(y[0], y[1]), pack_act<F16>(y[2], y[3]), pack_act<F16>(y[4], y[5]),
-                                   pack_act<F16>(y[6], y[7]));
-        if (ok && h + u < h1) *reinterpret_cast<uint4*>(out + (h + u) * (2 * D)) = o;
-      }
-    }
+    rotate_q<D, F16, 4>(p, blockIdx.x - kv_ctas);
     return;
   }
 
@@ -258,40 +278,52 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 1) cache_append_kernel(cons
   const int64_t sc0 = (page * p.c.page_blocks + (off >> p.c.block_shift)) * p.c.heads;
   const int64_t tok0 = page * p.c.page16 + off * p.c.token16;
   const int tw = in_team * kTeamRows + rsub;  // the lane's row of warp step i: tw + i * kRows
+  uint32_t in = 0;  // bit i: the lane's row of warp step i is new
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int t = tw + i * kRows<D>;
+    if (t >= lo && t < hi_ok) in |= 1u << i;
+  }
+  uint4 raw[kSteps];
+  auto load = [&](int job) {
+    const bool v = job >= p.c.heads;
+    const uint8_t* src = (v ? p.v : p.k) + (v ? job - p.c.heads : job) * (2 * D) + sub * 16 +
+                         (row0 + (t0 - past) + tw) * p.kv_stride;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i)
+      raw[i] = job < j1 && (in >> i & 1) ? __ldcs(reinterpret_cast<const uint4*>(src + i * kRows<D> * p.kv_stride))
+                                         : make_uint4(0, 0, 0, 0);
+  };
+  load(j0 + warp / team);
   for (int jb = j0; jb < j1; jb += teams) {
     const int job = jb + warp / team;
     const bool on = job < j1;
     const bool is_v = on && job >= p.c.heads;
     const int h = on ? (is_v ? job - p.c.heads : job) : 0;
-    const uint8_t* src = (is_v ? p.v : p.k) + h * (2 * D) + sub * 16 + (row0 + (t0 - past) + tw) * p.kv_stride;
-    uint4 raw[kSteps];
-    uint32_t in = 0;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int t = tw + i * kRows<D>;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (on && t >= lo && t < hi_ok) {
-        raw[i] = __ldcs(reinterpret_cast<const uint4*>(src + i * kRows<D> * p.kv_stride));
-        in |= 1u << i;
-      }
-    }
     float* sp = (is_v ? p.c.vs : p.c.ks) + sc0 + h;
     const float old = on && lo > 0 ? *sp : 0.f;
     RotView r = p.r;
     if (is_v) r.rot = 0;
-    float m = 0.f;
+    float m = 0.f, y[kSteps][8];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       Angles a;
-      float y[8];
       if ((in >> i & 1) && r.rot) load_angles(r, t0 + tw + i * kRows<D>, sub, a);
-      rotate<D, F16>(r, raw[i], sub, a, y);
+      rotate<D, F16>(r, raw[i], sub, a, y[i]);
+      float top = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = fabsf(y[e]);
-        if ((in >> i & 1) && v < INFINITY) m = fmaxf(m, v);
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[i][e]));  // (NaN passes by)
+      if (top == INFINITY) {  // infinite values become NaN, and do not count
+        top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (fabsf(y[i][e]) == INFINITY) y[i][e] = NAN;
+          top = fmaxf(top, fabsf(y[i][e]));
+        }
       }
+      if (in >> i & 1) m = fmaxf(m, top);
     }
+    load(job + teams);  // the next job's rows are on the way meanwhile
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
     if (team > 1) {
@@ -307,24 +339,22 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 1) cache_append_kernel(cons
     else
       __syncwarp();
     uint8_t* dst = (is_v ? p.c.v : p.c.k) + (tok0 + h * p.c.head16 + tw * p.c.token16) * 16 + sub * 8;
-    const float inv = 1.f / sc;  // a power of two: exact
+    const float inv = __uint_as_float((254u << 23) - __float_as_uint(sc));  // 1 / sc: a power of two
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int t = tw + i * kRows<D>;
       uint2* at = reinterpret_cast<uint2*>(dst + i * kRows<D> * p.c.token16 * 16);
-      Angles a;
-      float z[8];
-      if ((in >> i & 1) && r.rot) load_angles(r, t0 + t, sub, a);
-      rotate<D, F16>(r, raw[i], sub, a, z);
       if (in >> i & 1) {
+        if (on) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = fabsf(z[e]) < INFINITY ? z[e] * inv : NAN;
-        *at = pack_codes(z);
-      } else if (on && t < lo && sc != old) {
+          for (int e = 0; e < 8; ++e) y[i][e] *= inv;
+          *at = pack_codes(y[i]);
+        }
+      } else if (on && tw + i * kRows<D> < lo && sc != old) {
         // an earlier token of a block whose scale rises
         const float f = old * inv;
         const uint2 was = *at;
         const uint32_t ww[2] = {was.x, was.y};
+        float z[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t hh = e4m3x2_to_f16x2(static_cast<uint16_t>(ww[e >> 1] >> (16 * (e & 1))));
@@ -345,9 +375,10 @@ cudaError_t launch_rotate_quantise(const void* x, int64_t S, int H, int D, bool 
                                    uint32_t* status, int sms, cudaStream_t stream) {
   if (S == 0 || H == 0) return cudaSuccess;
   const int64_t bx = (S + 8 * (256 / D) - 1) / (8 * (256 / D));
-  // few tokens: the heads are split over CTAs until the SMs have two each
+  // the heads are split over CTAs until there are many for each place on the SMs
+  // (16,384 tokens: 119 us with 1,024 CTAs, @@ with 4,096)
   int split = 1;
-  while (bx * split < 2 * sms && split * 4 <= H) split *= 2;
+  while (bx * split < 16 * sms && split * 8 <= H) split *= 2;
   const int per = (H + split - 1) / split;
   const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>((H + per - 1) / per));
   const uint8_t* xb = static_cast<const uint8_t*>(x);
@@ -366,30 +397,51 @@ cudaError_t launch_rotate_quantise(const void* x, int64_t S, int H, int D, bool 
 cudaError_t launch_cache_append(AppendParams p, int D, bool f16, int sms, cudaStream_t stream) {
   if (p.s.S == 0 || p.s.B == 0) return cudaSuccess;
   p.kv_slots = static_cast<int32_t>(p.s.S / p.c.block + 2 * static_cast<int64_t>(p.s.B));
-  const int team_rows = kSteps * (256 / D), team = p.c.block <= team_rows ? 1 : p.c.block / team_rows;
+  const int steps = D == 128 && p.c.block == 128 ? 8 : 4;  // (a block of tokens is at most a CTA's)
+  const int team_rows = steps * (256 / D), team = p.c.block <= team_rows ? 1 : p.c.block / team_rows;
   const int teams = kAppendWarps / team;
   p.kv_split = 1;
-  while (static_cast<int64_t>(p.kv_slots) * p.kv_split < 2 * sms && p.kv_split * teams < 2 * p.c.heads) p.kv_split *= 2;
+  while (static_cast<int64_t>(p.kv_slots) * p.kv_split < 4 * sms && p.kv_split * teams < 2 * p.c.heads) p.kv_split *= 2;
   p.q_slots = p.q_heads = 0;
   int64_t q_ctas = 0;
   if (p.q) {
     const int cta_rows = kAppendWarps * (256 / D);
     p.q_slots = static_cast<int32_t>((p.s.S + cta_rows - 1) / cta_rows);
     int split = 1;
-    while (static_cast<int64_t>(p.q_slots) * split < 2 * sms && split * 4 <= p.Hq) split *= 2;
+    while (static_cast<int64_t>(p.q_slots) * split < 16 * sms && split * 8 <= p.Hq) split *= 2;
     p.q_heads = (p.Hq + split - 1) / split;
     q_ctas = static_cast<int64_t>(p.q_slots) * ((p.Hq + p.q_heads - 1) / p.q_heads);
   }
-  const int64_t grid = static_cast<int64_t>(p.kv_slots) * p.kv_split + q_ctas;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
-#define HWR_GO(DD, FF) cache_append_kernel<DD, FF><<<static_cast<unsigned>(grid), kAppendWarps * 32, 0, stream>>>(p)
-  if (D == 128) {
-    if (f16) HWR_GO(128, true); else HWR_GO(128, false);
+  // Small calls in one launch; q of 8,192 rows x 64 heads apart.  (8,192 tokens:
+  // 95 us in one, @@ us in two; 16 tokens: 8.3 and 10.4 us.)
+  p.q_apart = q_ctas >= 8 * sms && p.s.S >= 1024;
+  const int64_t grid = static_cast<int64_t>(p.kv_slots) * p.kv_split + (p.q_apart ? 0 : q_ctas);
+  if (grid > INT32_MAX || q_ctas > INT32_MAX) return cudaErrorInvalidValue;
+#define HWR_GO(DD, FF, SS) \
+  cache_append_kernel<DD, FF, SS><<<static_cast<unsigned>(grid), kAppendWarps * 32, 0, stream>>>(p)
+  if (D == 64) {
+    if (f16) HWR_GO(64, true, 4); else HWR_GO(64, false, 4);
+  } else if (steps == 4) {
+    if (f16) HWR_GO(128, true, 4); else HWR_GO(128, false, 4);
   } else {
-    if (f16) HWR_GO(64, true); else HWR_GO(64, false);
+    if (f16) HWR_GO(128, true, 8); else HWR_GO(128, false, 8);
   }
 #undef HWR_GO
-  return cudaGetLastError();
+  if (!p.q_apart) return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(q_ctas));
+  cfg.blockDim = dim3(kAppendWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (D == 64)
+    return f16 ? cudaLaunchKernelEx(&cfg, cache_q_kernel<64, true>, p) : cudaLaunchKernelEx(&cfg, cache_q_kernel<64, false>, p);
+  return f16 ? cudaLaunchKernelEx(&cfg, cache_q_kernel<128, true>, p) : cudaLaunchKernelEx(&cfg, cache_q_kernel<128, false>, p);
 }
 
 }  // namespace hwr
