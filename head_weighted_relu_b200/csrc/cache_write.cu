@@ -3,11 +3,10 @@
 // rotated keys and of values to a paged cache with a scale per block of tokens
 // and head.
 //
-// Both only move bytes.  A lane holds 8 consecutive dimensions (a 16-byte
-// load), so a row of D takes D/8 lanes and a warp step 256/D rows.  The
-// rotation's partner dimensions of the half-split layout lie a whole number of
-// lanes away (rot_dim is a multiple of 16) and come by shuffle; those of the
-// interleaved layout are the lane's own.
+// Both only move bytes.  A lane holds 8 dimensions, so a row of D takes D/8
+// lanes and a warp step 256/D rows: two groups of four, which in the rotated
+// part of the half-split layout are four dimensions and their partners (so no
+// lane needs another's values), elsewhere eight in a row.
 #include "cache.h"
 
 namespace hwr {
@@ -18,75 +17,69 @@ constexpr int kLanes = D / 8;      // lanes of a row
 template <int D>
 constexpr int kRows = 256 / D;     // rows of a warp step
 
-// Cosines and sines that a lane needs for its 8 dimensions at one position.
-struct Angles {
-  float c[8], s[8];
+// First dimensions of the two groups of four of lane `sub` of a row.
+struct Dims {
+  int lo, hi;
 };
-
-// sub: the lane's index within its row.  Interleaved: entry i serves the pair (2i, 2i+1).
-__device__ __forceinline__ void load_angles(const RotView& r, int64_t pos, int sub, Angles& a) {
-  const int half = r.rot >> 1;
-  if (8 * sub >= r.rot) return;
-  const float* row = r.table + pos * r.rot;
-  if (r.inter) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(row + 4 * sub));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + 4 * sub));
-    a.c[0] = c.x, a.c[1] = c.y, a.c[2] = c.z, a.c[3] = c.w;
-    a.s[0] = s.x, a.s[1] = s.y, a.s[2] = s.z, a.s[3] = s.w;
-  } else {
-    const int d = 8 * sub < half ? 8 * sub : 8 * sub - half;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + d + 4 * i));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + d + 4 * i));
-      a.c[4 * i] = c.x, a.c[4 * i + 1] = c.y, a.c[4 * i + 2] = c.z, a.c[4 * i + 3] = c.w;
-      a.s[4 * i] = s.x, a.s[4 * i + 1] = s.y, a.s[4 * i + 2] = s.z, a.s[4 * i + 3] = s.w;
-    }
-  }
+__device__ __forceinline__ Dims lane_dims(const RotView& r, int sub) {
+  if (!r.inter && 8 * sub < r.rot) return Dims{4 * sub, (r.rot >> 1) + 4 * sub};
+  return Dims{8 * sub, 8 * sub + 4};
 }
 
-// The 8 values of `raw` in FP32, rotated.  Every product and sum is rounded on
-// its own (no contraction), so the result is that of the formula in FP32.
-// All 32 lanes take part.
-template <int D, bool F16>
-__device__ __forceinline__ void rotate(const RotView& r, const uint4& raw, int sub, const Angles& a, float (&y)[8]) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack_act<F16>(w[i]);
-    y[2 * i] = f.x, y[2 * i + 1] = f.y;
-  }
-  if (r.rot == 0) return;
-  if (r.inter) {
-    if (8 * sub < r.rot) {
+// Cosines and sines of a lane's four pairs at one position.
+struct Angles {
+  float2 c[2], s[2];
+};
+__device__ __forceinline__ void load_angles(const RotView& r, int64_t pos, int sub, Angles& a) {
+  if (8 * sub >= r.rot) return;
+  const float* row = r.table + pos * r.rot + 4 * sub;
+  const float4 c = __ldg(reinterpret_cast<const float4*>(row));
+  const float4 s = __ldg(reinterpret_cast<const float4*>(row + (r.rot >> 1)));
+  a.c[0] = make_float2(c.x, c.y), a.c[1] = make_float2(c.z, c.w);
+  a.s[0] = make_float2(s.x, s.y), a.s[1] = make_float2(s.z, s.w);
+}
+
+struct Raw {
+  uint2 lo, hi;
+};
+__device__ __forceinline__ Raw no_row() { return Raw{make_uint2(0, 0), make_uint2(0, 0)}; }
+__device__ __forceinline__ Raw load_row(const uint8_t* row, const Dims& d) {
+  return Raw{__ldcs(reinterpret_cast<const uint2*>(row + 2 * d.lo)), __ldcs(reinterpret_cast<const uint2*>(row + 2 * d.hi))};
+}
+
+// The lane's values in FP32, rotated: y[0, 4) of the first group, y[4, 8) of the
+// second.  Every product and sum is rounded on its own (no contraction), so the
+// result is that of the formula in FP32.  PACKED: products two at a time (16,384
+// x 64 rows 100 us, 107 without; the append 74 us, 70 without).
+template <bool F16, bool PACKED>
+__device__ __forceinline__ void rotate(const RotView& r, const Raw& raw, int sub, const Angles& a, float (&y)[8]) {
+  float2 p[2] = {unpack_act<F16>(raw.lo.x), unpack_act<F16>(raw.lo.y)};
+  float2 q[2] = {unpack_act<F16>(raw.hi.x), unpack_act<F16>(raw.hi.y)};
+  if (8 * sub < r.rot) {
+    if (r.inter) {  // pairs (x, y) of each float2
+      float2* v[4] = {&p[0], &p[1], &q[0], &q[1]};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float p = y[2 * i], q = y[2 * i + 1];
-        y[2 * i] = __fsub_rn(__fmul_rn(p, a.c[i]), __fmul_rn(q, a.s[i]));
-        y[2 * i + 1] = __fadd_rn(__fmul_rn(q, a.c[i]), __fmul_rn(p, a.s[i]));
+        const float c = i & 1 ? a.c[i / 2].y : a.c[i / 2].x, s = i & 1 ? a.s[i / 2].y : a.s[i / 2].x, x = v[i]->x, z = v[i]->y;
+        *v[i] = make_float2(__fsub_rn(__fmul_rn(x, c), __fmul_rn(z, s)), __fadd_rn(__fmul_rn(z, c), __fmul_rn(x, s)));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // (the sums not in pairs: a packed sum of packed products becomes one FMA)
+        auto times = [](float2 a, float2 b) {
+          return PACKED ? mul2(a, b) : make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y));
+        };
+        const float2 pc = times(p[i], a.c[i]), qs = times(q[i], a.s[i]), qc = times(q[i], a.c[i]), ps = times(p[i], a.s[i]);
+        p[i] = make_float2(__fsub_rn(pc.x, qs.x), __fsub_rn(pc.y, qs.y));
+        q[i] = make_float2(__fadd_rn(qc.x, ps.x), __fadd_rn(qc.y, ps.y));
       }
     }
-    return;
   }
-  const int hl = r.rot >> 4;  // lanes between the two halves
-  const int lane = threadIdx.x & 31;
-  const bool first = sub < hl;
-  const bool in = sub < 2 * hl;
-  const int from = in ? (first ? lane + hl : lane - hl) : lane;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t o = __shfl_sync(kFullMask, w[i], from);
-    const float2 f = unpack_act<F16>(o);
-    const float pv[2] = {f.x, f.y};
-    if (in) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int e = 2 * i + j;
-        const float xc = __fmul_rn(y[e], a.c[e]), os = __fmul_rn(pv[j], a.s[e]);
-        // first half: a cos - b sin; second: b cos + a sin
-        y[e] = first ? __fsub_rn(xc, os) : __fadd_rn(xc, os);
-      }
-    }
+  for (int i = 0; i < 2; ++i) {
+    y[2 * i] = p[i].x, y[2 * i + 1] = p[i].y;
+    y[4 + 2 * i] = q[i].x, y[5 + 2 * i] = q[i].y;
   }
 }
 
@@ -97,6 +90,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// (of the two groups)
 __device__ __forceinline__ uint2 pack_codes(const float (&y)[8]) {
   uint2 r;
   r.x = f32x2_to_e4m3x2(y[0], y[1]) | (f32x2_to_e4m3x2(y[2], y[3]) << 16);
@@ -124,18 +118,17 @@ __global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __r
     if (ok) load_angles(rot, pos, sub, a);
     if (!ok && sub == 0 && h0 == 0 && status) atomicOr(status, kStatusToken);
   }
-  const uint8_t* row = x + t * x_stride + sub * 16;
+  const Dims d = lane_dims(rot, sub);
+  const uint8_t* row = x + t * x_stride;
   constexpr int U = 4;
   for (int h = h0; h < h1; h += U) {
-    uint4 raw[U];
+    Raw raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      raw[u] = ok && h + u < h1 ? __ldcs(reinterpret_cast<const uint4*>(row + (h + u) * (2 * D)))
-                                : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < U; ++u) raw[u] = ok && h + u < h1 ? load_row(row + (h + u) * (2 * D), d) : no_row();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float y[8];
-      rotate<D, F16>(rot, raw[u], sub, a, y);
+      rotate<F16, true>(rot, raw[u], sub, a, y);
       float m = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
@@ -155,9 +148,10 @@ __global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __r
       if (__all_sync(kFullMask, plain)) {
         const float inv = __frcp_rn(sc);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float q = y[i] * inv;
-          z[i] = fmaf(fmaf(-q, sc, y[i]), inv, q);
+        for (int i = 0; i < 8; i += 2) {
+          const float2 v = make_float2(y[i], y[i + 1]), r2 = make_float2(inv, inv);
+          const float2 q = mul2(v, r2), w = fma2(fma2(q, make_float2(-sc, -sc), v), r2, q);
+          z[i] = w.x, z[i + 1] = w.y;
         }
       } else {
         sc = m == 0.f ? 1.f : __fdiv_rn(m, 448.f);
@@ -167,7 +161,8 @@ __global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __r
       const uint2 code = pack_codes(z);
       if (live && h + u < h1) {
         const int64_t o = t * H + h + u;
-        *reinterpret_cast<uint2*>(codes + o * D + sub * 8) = code;
+        *reinterpret_cast<uint32_t*>(codes + o * D + d.lo) = code.x;
+        *reinterpret_cast<uint32_t*>(codes + o * D + d.hi) = code.y;
         if (sub == 0) scale[o] = ok ? sc : 1.f;
       }
     }
@@ -208,21 +203,22 @@ __device__ __forceinline__ void rotate_q(const AppendParams& p, int i) {
     if (ok && p.r.rot) load_angles(p.r, pos, sub, a);
     if (!ok && sub == 0 && h0 == 0 && p.status) atomicOr(p.status, kStatusToken);
   }
-  const uint8_t* in = p.q + r * p.q_stride + sub * 16;
-  uint8_t* out = p.q_out + (static_cast<int64_t>(r) * p.Hq) * (2 * D) + sub * 16;
+  const Dims d = lane_dims(p.r, sub);
+  const uint8_t* in = p.q + r * p.q_stride;
+  uint8_t* out = p.q_out + (static_cast<int64_t>(r) * p.Hq) * (2 * D);
   for (int h = h0; h < h1; h += U) {
-    uint4 raw[U];
+    Raw raw[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      raw[u] = ok && h + u < h1 ? __ldcs(reinterpret_cast<const uint4*>(in + (h + u) * (2 * D)))
-                                : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < U; ++u) raw[u] = ok && h + u < h1 ? load_row(in + (h + u) * (2 * D), d) : no_row();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float y[8];
-      rotate<D, F16>(p.r, raw[u], sub, a, y);
-      const uint4 o = make_uint4(pack_act<F16>(y[0], y[1]), pack_act<F16>(y[2], y[3]), pack_act<F16>(y[4], y[5]),
-                                 pack_act<F16>(y[6], y[7]));
-      if (ok && h + u < h1) *reinterpret_cast<uint4*>(out + (h + u) * (2 * D)) = o;
+      rotate<F16, false>(p.r, raw[u], sub, a, y);
+      if (ok && h + u < h1) {
+        uint8_t* to = out + (h + u) * (2 * D);
+        *reinterpret_cast<uint2*>(to + 2 * d.lo) = make_uint2(pack_act<F16>(y[0], y[1]), pack_act<F16>(y[2], y[3]));
+        *reinterpret_cast<uint2*>(to + 2 * d.hi) = make_uint2(pack_act<F16>(y[4], y[5]), pack_act<F16>(y[6], y[7]));
+      }
     }
   }
 }
@@ -230,8 +226,8 @@ __device__ __forceinline__ void rotate_q(const AppendParams& p, int i) {
 // q of many rows, beside the kernel for keys and values: with its registers (two
 // CTAs an SM) the copy would wait for memory.
 template <int D, bool F16>
-__global__ void __launch_bounds__(kAppendWarps * 32, 5) cache_q_kernel(const __grid_constant__ AppendParams p) {
-  rotate_q<D, F16, 2>(p, blockIdx.x);
+__global__ void __launch_bounds__(kAppendWarps * 32, 4) cache_q_kernel(const __grid_constant__ AppendParams p) {
+  rotate_q<D, F16, 4>(p, blockIdx.x);
   // complete no earlier than the kernel that this one did not wait for
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -284,15 +280,15 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) cache_append_k
     const int t = tw + i * kRows<D>;
     if (t >= lo && t < hi_ok) in |= 1u << i;
   }
-  uint4 raw[kSteps];
+  const Dims d = lane_dims(p.r, sub);
+  Raw raw[kSteps];
   auto load = [&](int job) {
     const bool v = job >= p.c.heads;
-    const uint8_t* src = (v ? p.v : p.k) + (v ? job - p.c.heads : job) * (2 * D) + sub * 16 +
+    const uint8_t* src = (v ? p.v : p.k) + (v ? job - p.c.heads : job) * (2 * D) +
                          (row0 + (t0 - past) + tw) * p.kv_stride;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
-      raw[i] = job < j1 && (in >> i & 1) ? __ldcs(reinterpret_cast<const uint4*>(src + i * kRows<D> * p.kv_stride))
-                                         : make_uint4(0, 0, 0, 0);
+      raw[i] = job < j1 && (in >> i & 1) ? load_row(src + i * kRows<D> * p.kv_stride, d) : no_row();
   };
   load(j0 + warp / team);
   for (int jb = j0; jb < j1; jb += teams) {
@@ -309,7 +305,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) cache_append_k
     for (int i = 0; i < kSteps; ++i) {
       Angles a;
       if ((in >> i & 1) && r.rot) load_angles(r, t0 + tw + i * kRows<D>, sub, a);
-      rotate<D, F16>(r, raw[i], sub, a, y[i]);
+      rotate<F16, false>(r, raw[i], sub, a, y[i]);
       float top = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[i][e]));  // (NaN passes by)
@@ -338,22 +334,24 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) cache_append_k
       __syncthreads();
     else
       __syncwarp();
-    uint8_t* dst = (is_v ? p.c.v : p.c.k) + (tok0 + h * p.c.head16 + tw * p.c.token16) * 16 + sub * 8;
+    uint8_t* dst = (is_v ? p.c.v : p.c.k) + (tok0 + h * p.c.head16 + tw * p.c.token16) * 16;
     const float inv = __uint_as_float((254u << 23) - __float_as_uint(sc));  // 1 / sc: a power of two
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      uint2* at = reinterpret_cast<uint2*>(dst + i * kRows<D> * p.c.token16 * 16);
+      uint8_t* to = dst + i * kRows<D> * p.c.token16 * 16;
+      uint32_t* lo4 = reinterpret_cast<uint32_t*>(to + d.lo);
+      uint32_t* hi4 = reinterpret_cast<uint32_t*>(to + d.hi);
       if (in >> i & 1) {
         if (on) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[i][e] *= inv;
-          *at = pack_codes(y[i]);
+          const uint2 code = pack_codes(y[i]);
+          *lo4 = code.x, *hi4 = code.y;
         }
       } else if (on && tw + i * kRows<D> < lo && sc != old) {
         // an earlier token of a block whose scale rises
         const float f = old * inv;
-        const uint2 was = *at;
-        const uint32_t ww[2] = {was.x, was.y};
+        const uint32_t ww[2] = {*lo4, *hi4};
         float z[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -361,7 +359,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) cache_append_k
           const float2 v = unpack_act<true>(hh);
           z[2 * e] = v.x * f, z[2 * e + 1] = v.y * f;
         }
-        *at = pack_codes(z);
+        const uint2 code = pack_codes(z);
+        *lo4 = code.x, *hi4 = code.y;
       }
     }
     if (on && lane == 0 && in_team == 0) *sp = sc;
@@ -376,7 +375,7 @@ cudaError_t launch_rotate_quantise(const void* x, int64_t S, int H, int D, bool 
   if (S == 0 || H == 0) return cudaSuccess;
   const int64_t bx = (S + 8 * (256 / D) - 1) / (8 * (256 / D));
   // the heads are split over CTAs until there are many for each place on the SMs
-  // (16,384 tokens: 119 us with 1,024 CTAs, @@ with 4,096)
+  // (16,384 tokens: 119 us with 1,024 CTAs, 117 with 4,096)
   int split = 1;
   while (bx * split < 16 * sms && split * 8 <= H) split *= 2;
   const int per = (H + split - 1) / split;
@@ -412,9 +411,10 @@ cudaError_t launch_cache_append(AppendParams p, int D, bool f16, int sms, cudaSt
     p.q_heads = (p.Hq + split - 1) / split;
     q_ctas = static_cast<int64_t>(p.q_slots) * ((p.Hq + p.q_heads - 1) / p.q_heads);
   }
-  // Small calls in one launch; q of 8,192 rows x 64 heads apart.  (8,192 tokens:
-  // 95 us in one, @@ us in two; 16 tokens: 8.3 and 10.4 us.)
-  p.q_apart = q_ctas >= 8 * sms && p.s.S >= 1024;
+  // q in a launch of its own where it is large: 8,192 rows x 64 heads x 128 (2^26
+  // values) take 95 us in one launch and 92 in two, 2,450 x 16 x 64 (2^21) 8.3
+  // and 10.3 us.
+  p.q_apart = p.q && p.s.S * p.Hq * D >= (int64_t(1) << 24);
   const int64_t grid = static_cast<int64_t>(p.kv_slots) * p.kv_split + (p.q_apart ? 0 : q_ctas);
   if (grid > INT32_MAX || q_ctas > INT32_MAX) return cudaErrorInvalidValue;
 #define HWR_GO(DD, FF, SS) \

@@ -69,6 +69,58 @@ def test_rotate_quantise(cuda_ok, S, H, D, act, rot, inter):
         assert torch.equal(codes.cpu(), (xf / s2[..., None]).to(torch.float8_e4m3fn).view(torch.uint8))
 
 
+@pytest.mark.parametrize("act,D,rot,inter", [("bf16", 128, 128, False), ("bf16", 128, 64, False), ("fp16", 64, 64, True),
+                                             ("fp16", 128, 48, False), ("bf16", 64, 16, True)])
+def test_rotation_rounds_each_product_on_its_own(cuda_ok, act, D, rot, inter):
+    """Rotated q and FP8 rows bit for bit as the formula in FP32, no product fused
+    with the sum (which the CPU's separate operations do not do either)."""
+    I = _I()
+    S, H = 300, 5
+    g = torch.Generator().manual_seed(rot)
+    x = torch.randn(S, H, D, generator=g).to(ACT[act])
+    rt = I.rope_table(S, rot)
+    c, s = rt.cpu()[:, None].split(rot // 2, dim=-1)
+    xf = x.float()
+    y = xf.clone()
+    a, b = (xf[..., 0:rot:2], xf[..., 1:rot:2]) if inter else (xf[..., :rot // 2], xf[..., rot // 2:rot])
+    ra, rb = a * c - b * s, b * c + a * s
+    if inter:
+        y[..., 0:rot:2], y[..., 1:rot:2] = ra, rb
+    else:
+        y[..., :rot // 2], y[..., rot // 2:rot] = ra, rb
+    cache = I.allocate_cache(1, 512, 1, D, 16)
+    k = torch.zeros(S, 1, D, dtype=ACT[act], device="cuda")
+    cu, kv = _dev(np.array([0, S], dtype=np.int32)), _dev(np.array([S], dtype=np.int32))
+    q = I.cache_append(cache, k, k, cu, kv, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), table=rt,
+                       interleaved=inter, q=x.cuda())
+    assert torch.equal(q.cpu(), y.to(ACT[act]))
+    codes, scale = I.rotate_quantise(x.cuda(), None, rt, interleaved=inter)
+    want = y.abs().amax(-1) / 448
+    assert torch.equal(scale.cpu(), want)
+    assert torch.equal(codes.cpu(), (y / want[..., None]).to(torch.float8_e4m3fn).view(torch.uint8))
+
+
+def test_append_of_many_rows(cuda_ok):
+    """Large enough for q to go through a kernel of its own: the same rows as in
+    pieces, and the cache with them."""
+    I = _I()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    S, Hq, heads, D = 2200, 64, 2, 128
+    q, k, v = (torch.randn(S, n, D, generator=g, device="cuda").bfloat16() for n in (Hq, heads, heads))
+    rt = I.rope_table(S, 128)
+    table = torch.arange(18, dtype=torch.int32, device="cuda").flip(0).view(1, 18)
+    one, two = (I.allocate_cache(18, 128, heads, D, 128) for _ in range(2))
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    whole = I.cache_append(one, k, v, ints(0, S), ints(S), table, table=rt, q=q)
+    parts = [I.cache_append(two, k[a:b], v[a:b], ints(0, b - a), ints(b), table, table=rt, q=q[a:b])
+             for a, b in ((0, 128), (128, 1024), (1024, 2048), (2048, S))]
+    assert torch.equal(whole, torch.cat(parts))
+    used = [i for i in range(18)][::-1]
+    for pg, n in ((p, min(128, S - 128 * i)) for i, p in enumerate(used)):
+        assert torch.equal(one.k[pg, :n], two.k[pg, :n]) and torch.equal(one.v[pg, :n], two.v[pg, :n])
+    assert torch.equal(one.k_scale, two.k_scale) and torch.equal(one.v_scale, two.v_scale)
+
+
 def test_rotate_quantise_bad_rows(cuda_ok):
     I = _I()
     x = torch.randn(6, 2, 64, device="cuda").bfloat16()
