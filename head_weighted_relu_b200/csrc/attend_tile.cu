@@ -173,7 +173,7 @@ __device__ __forceinline__ void look_up(const AttendParams& p, const Segment& g,
     Translate::Place at[kPer];
     float ks[kPer], vs[kPer];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) ix[e] = tr.index((g.u0 + j) * kKeys + (U16 ? en * 16 : e * 32 + en));
+    for (int e = 0; e < kPer; ++e) ix[e] = tr.index(j < g.n ? (g.u0 + j) * kKeys + (U16 ? en * 16 : e * 32 + en) : -1);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) pg[e] = tr.page(ix[e]);
 #pragma unroll

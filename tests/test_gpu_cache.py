@@ -377,6 +377,7 @@ ATTENDS = [
     ([150], [2900], 6, 2, 128, 48, 4, "bf16", True, False),
     ([70], [3100], 8, 2, 128, 128, 64, "fp16", True, True),
     ([1], [1], 64, 1, 64, 16, 16, "bf16", True, False),
+    ([5] * 20, list(range(5, 605, 30)), 64, 64, 64, 16, 16, "bf16", True, False),     # a CTA for each (tile, head)
 ]
 
 
@@ -533,6 +534,51 @@ def test_attend_passes_over_bad_pages(cuda_ok, kernel):
     assert status.item() == I.STATUS_TOKEN
     _check_attend(cache, q, cu, kv, t2, 64 ** -0.5, True, None, out, lse, "bf16")
     assert (out[2] == 0).all()
+
+
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+def test_attend_calls_at_once_and_rows_on_their_own(cuda_ok, kernel):
+    """Two calls side by side on two streams, with a workspace each; and a row's
+    result in a batch is that of the row alone where its keys are divided alike."""
+    I = _I()
+    rng = np.random.default_rng(21)
+    kv = [4000, 250, 3500, 1]
+    cache, table = _filled(rng, kv, 1, 128, 64, 16)
+    cu, n, tb = _dev(np.arange(5, dtype=np.int32)), _dev(np.array(kv, dtype=np.int32)), _dev(table)
+    qs = [_dev(rng.normal(size=(4, 24, 128)), torch.bfloat16) for _ in range(2)]
+    want = [I.cache_attend(cache, q, cu, n, tb, kernel=kernel) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in qs]
+    for _ in range(20):
+        for i, (q, s) in enumerate(zip(qs, streams)):
+            got[i].append(I.cache_attend(cache, q, cu, n, tb, kernel=kernel, stream=s))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
+    # other queries in the batch change nothing of a row
+    mixed = qs[0].clone()
+    mixed[[0, 2]] = qs[1][[0, 2]] * 50
+    out = I.cache_attend(cache, mixed, cu, n, tb, kernel=kernel)
+    assert torch.equal(out[[1, 3]], want[0][[1, 3]])
+
+
+def test_attend_in_large_prefill(cuda_ok):
+    """More tiles than CTAs share: against the same rows in pieces."""
+    I = _I()
+    rng = np.random.default_rng(22)
+    n, Hq, heads, D = 1500, 32, 32, 64
+    cache, table = _filled(rng, [n], heads, D, 64, 64)
+    q = _dev(rng.normal(size=(n, Hq, D)), torch.bfloat16)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    whole = I.cache_attend(cache, q, ints(0, n), ints(n), _dev(table), kernel=TILE)
+    for a in (0, 700, 1400):
+        part = I.cache_attend(cache, q[a:a + 100].contiguous(), ints(0, 100), ints(a + 100), _dev(table), kernel=STREAM)
+        x, y = whole[a:a + 100].float(), part.float()
+        # both within the tolerance of their own: a rounding of the output's type, of
+        # FP16 weights, and of FP32 scores, each of values no larger than the row's largest
+        assert (x - y).abs().max() <= 2 * (2.0 ** -8 + 2.0 ** -10) * y.abs().max()
 
 
 def test_attend_shares_pages_between_sequences(cuda_ok):
