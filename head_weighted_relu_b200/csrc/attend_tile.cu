@@ -17,6 +17,22 @@
 // reference of a row's exponentials rises only when a score exceeds it by
 // kSlack, which is rare after the first tile; then the row's outputs are
 // rescaled in TMEM.
+//
+// What bounds it (D = 128, two streams).  A tile of 128 keys is 2,048 clocks of
+// products for 256 rows (32 of 128x128x16, 64 clocks each), 2,048 of
+// exponentials (16 a clock and SM), about 1,000 of the integer pipe (conversions,
+// maxima) and 2,000 of shared memory; measured are about 4,700: a stream's
+// softmax (2,100 alone, 2,800 beside the other's, 3,000 to 3,400 beside the
+// fill) and its products (1,100 and the hand-overs) follow one another, and two
+// streams do not cover all of each other.  2,048 rows over 16,384 tokens, 64
+// heads on 8: 1.18 ms, 875 TFLOP/s.  One stream's rows, NM = 1: one query of 64
+// heads over 1,048,576 tokens 109 us, 2.5 TB/s.
+// Tried and worse: scores in halves of 64 keys, so that products run during the
+// softmax (the halves' products re-read the queries: 1.34 ms); one pass that
+// keeps the weights in registers, or takes no maximum until a sum overflows (1.35
+// ms: longer code or spilled registers, which meet a small instruction cache and
+// the L1 that shared memory leaves); issuing products inside one lane's branch
+// (130 clocks each instead of 67).
 #include "attend.cuh"
 #include "internal.h"
 

@@ -470,6 +470,7 @@ indexer_status indexer_cache_append(const indexer_cache* cache, const indexer_se
  * Tokens whose page lies outside the cache or the page table are not seen
  * and set bit 3 of *status.  What the cache holds elsewhere than at seen
  * positions never matters.
+ * Calls with the same shapes and contents give the same bits.
  * Scores, softmax statistics and sums are FP32; the probabilities are
  * rounded to FP16 (relative to the largest seen, with 2^-31 of it as the least),
  * as a factor of the value products only.  The value scales
