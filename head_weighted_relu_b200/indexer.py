@@ -485,25 +485,35 @@ def _device_of(x):
     return i
 
 
+# The current device and its stream's handle, without the objects around them
+# (a few microseconds of a decode step's call).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _call(fn, device, stream, *args):
     """lib.fn(*args, stream) with `device` current, on the caller's stream or the
     device's current one."""
-    if torch.cuda.current_device() == device:
-        status = getattr(_lib, fn)(*args, (stream or torch.cuda.current_stream(device)).cuda_stream)
+    if _current_device() == device:
+        status = getattr(_lib, fn)(*args, _current_stream(device) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            status = getattr(_lib, fn)(*args, (stream or torch.cuda.current_stream(device)).cuda_stream)
+            status = getattr(_lib, fn)(*args, _current_stream(device) if stream is None else stream.cuda_stream)
     if status != 0:
         raise IndexerError(fn, status)
 
 
-def _new(stream, device, shape, dtype):
-    """An uninitialised tensor for the call: on the call's stream, so that its
-    memory is not handed to other work while the call may still use it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _new(stream, like, shape, dtype):
+    """An uninitialised tensor for the call, on the device of `like`: on the call's
+    stream, so that its memory is not handed to other work while the call may
+    still use it.  shape None: that of `like`."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _new(None, like, shape, dtype)
+    if shape is None:
+        return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
+    return like.new_empty(shape, dtype=dtype)
 
 
 def rope_table(positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
@@ -534,8 +544,8 @@ def rotate_quantise(x, positions=None, table=None, interleaved=False, out=None, 
     rot = _rotation(table, interleaved, device)
     pos = None if positions is None else _ints(positions, "positions", device, (S,))
     if out is None:
-        codes = _new(stream, device, shape, torch.uint8)
-        scale = _new(stream, device, (S, H), torch.float32)
+        codes = _new(stream, x, None, torch.uint8)
+        scale = _new(stream, x, (S, H), torch.float32)
     else:
         codes, scale = out
         if not (codes.dtype in _CODES and codes.is_contiguous() and codes.numel() == S * H * D
@@ -626,7 +636,7 @@ def cache_append(cache: KVCache, k, v, cu_q, kv_len, page_table, table=None, int
         q_heads = shape[1] if len(shape) == 3 else 0
         q_stride = _tokens(q, "q", device, (S, q_heads, desc.D), dtype)
         if q_out is None:
-            q_out = _new(stream, device, shape, dtype)
+            q_out = _new(stream, q, None, dtype)
         else:
             _result(q_out, "q_out", device, shape, dtype)
         qp, qo = q.data_ptr(), q_out.data_ptr()
@@ -670,14 +680,14 @@ def cache_attend(cache: KVCache, q, cu_q, kv_len, page_table, scale=None, causal
     att = Attention(Hq, act, 1 if causal else 0, width, max_q, scale if scale is not None else 1 / math.sqrt(desc.D),
                     kernel)
     if workspace is None:
-        workspace = _new(stream, device, (_attend_workspace(device, desc, seqs, att),), torch.uint8)
+        workspace = _new(stream, q, (_attend_workspace(device, desc, seqs, att),), torch.uint8)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on cuda:{device}")
     if out is None:
-        out = _new(stream, device, shape, dtype)
+        out = _new(stream, q, None, dtype)
     else:
         _result(out, "out", device, shape, dtype)
-    lse = _new(stream, device, (S, Hq), torch.float32) if with_lse else None
+    lse = _new(stream, q, (S, Hq), torch.float32) if with_lse else None
     _call("indexer_cache_attend", device, stream, desc, seqs, att, q.data_ptr(), stride, si, sl, out.data_ptr(),
           None if lse is None else lse.data_ptr(),
           None if status is None else _ints(status, "status", device, (1,)), workspace.data_ptr(),
@@ -685,15 +695,23 @@ def cache_attend(cache: KVCache, q, cu_q, kv_len, page_table, scale=None, causal
     return (out, lse) if with_lse else out
 
 
+_attend_sizes = {}   # workspace bytes by what they depend on: the device and the shapes
+
+
 def _attend_workspace(device, desc, seqs, att) -> int:
+    key = (device, desc.heads, desc.D, desc.page_size, desc.block, seqs.S, seqs.B, seqs.table_pages, att.Hq, att.act,
+           att.sel_width, att.max_q, att.kernel)
+    size = _attend_sizes.get(key)
+    if size is not None:
+        return size
     n = ctypes.c_size_t()
-    if torch.cuda.current_device() == device:
+    with torch.cuda.device(device):
         status = _lib.indexer_cache_attend_workspace_bytes(desc, seqs, att, n)
-    else:
-        with torch.cuda.device(device):
-            status = _lib.indexer_cache_attend_workspace_bytes(desc, seqs, att, n)
     if status != 0:
         raise IndexerError("indexer_cache_attend_workspace_bytes", status)
+    if len(_attend_sizes) >= 4096:
+        _attend_sizes.clear()
+    _attend_sizes[key] = n.value
     return n.value
 
 
