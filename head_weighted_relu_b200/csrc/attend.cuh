@@ -49,6 +49,7 @@ struct AttendParams {
   int32_t n_tiles;         // tile slots
   int32_t sel_tiles;       // tiles of one query (selection)
   int32_t n_ctas;          // CTAs that share the units, or 0: one CTA per (tile, head)
+  int32_t lanes;           // CTAs side by side on the same keys, one a head; or 1
   JoinJob* jobs;           // [n_ctas] (workspace)
   float* part_o;           // [2 n_ctas][rows][D]
   float2* part_ml;         // [2 n_ctas][rows]: reference and sum
@@ -121,8 +122,29 @@ __device__ __forceinline__ int row_limit(const AttendParams& p, const Tile& x, i
 template <int UNIT, int THREADS>
 __device__ __forceinline__ int tile_prefix(const AttendParams& p, int R, int* prefix, int* warp_sums);
 
-// CTA c of n <= u takes units [start(c), start(c+1)) of u: one or more each.
-__host__ __device__ __forceinline__ int64_t share_start(int64_t c, int64_t u, int64_t n) { return c * u / n; }
+// How CTAs share units.  With lanes = 1, those of all heads in a row, head by
+// head.  With lanes = heads, CTAs c, c + 1, .. stand for heads 0, 1, .. of the
+// same keys, and `lanes` shares of the units of one head: heads lie beside one
+// another in the cache, and read together they are read in longer pieces.
+struct Share {
+  int64_t units, n, start, end;  // of these units, n shares; this CTA's
+  int heads, h;                  // heads among the units, and the head they begin with
+};
+__device__ __forceinline__ int64_t share_start(int64_t c, int64_t u, int64_t n);
+__device__ __forceinline__ Share share_of(const AttendParams& p, int total) {
+  Share s;
+  s.heads = p.lanes > 1 ? 1 : p.c.heads;
+  s.h = blockIdx.x % p.lanes;
+  s.units = static_cast<int64_t>(total) * s.heads;
+  s.n = min(s.units, static_cast<int64_t>(p.n_ctas / p.lanes));
+  const int64_t c = blockIdx.x / p.lanes;
+  s.start = c < s.n ? share_start(c, s.units, s.n) : 0;
+  s.end = c < s.n ? share_start(c + 1, s.units, s.n) : 0;
+  return s;
+}
+
+// Share c of n <= u is units [start(c), start(c+1)) of u: one or more each.
+__device__ __forceinline__ int64_t share_start(int64_t c, int64_t u, int64_t n) { return c * u / n; }
 __device__ __forceinline__ int64_t share_owner(int64_t unit, int64_t u, int64_t n) {
   return ((unit + 1) * n - 1) / u;
 }
@@ -132,21 +154,21 @@ struct Piece {
   int tile, h, u0, u1;
   bool whole;  // all of the (tile, head)'s units
 };
-__device__ __forceinline__ int tile_of(const AttendParams& p, const int* prefix, int64_t u) {
+__device__ __forceinline__ int tile_of(const AttendParams& p, const int* prefix, int heads, int64_t u) {
   int lo = 0, hi = p.n_tiles - 1;  // the last tile that starts at or before u (empty ones start with the next)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(prefix[mid]) * p.c.heads <= u) lo = mid; else hi = mid - 1;
+    if (static_cast<int64_t>(prefix[mid]) * heads <= u) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
-__device__ __forceinline__ Piece piece_at(const AttendParams& p, const int* prefix, int64_t u, int64_t end) {
-  const int lo = tile_of(p, prefix, u);
+__device__ __forceinline__ Piece piece_at(const AttendParams& p, const int* prefix, const Share& sh, int64_t u, int64_t end) {
+  const int lo = tile_of(p, prefix, sh.heads, u);
   const int tu = prefix[lo + 1] - prefix[lo];
-  const int64_t in = u - static_cast<int64_t>(prefix[lo]) * p.c.heads;
+  const int64_t in = u - static_cast<int64_t>(prefix[lo]) * sh.heads;
   Piece r;
   r.tile = lo;
-  r.h = static_cast<int>(in / tu);
+  r.h = sh.h + static_cast<int>(in / tu);
   r.u0 = static_cast<int>(in % tu);
   r.u1 = static_cast<int>(min(static_cast<int64_t>(tu), r.u0 + (end - u)));
   r.whole = r.u0 == 0 && r.u1 == tu;
@@ -277,19 +299,18 @@ __device__ __forceinline__ int tile_prefix(const AttendParams& p, int R, int* pr
   return total;
 }
 
-// Notes this CTA's job for the join; [start, end) is its share of `units`.  One thread.
-__device__ __forceinline__ void note_job(const AttendParams& p, int R, const int* prefix, int64_t units,
-                                         int64_t start, int64_t end) {
+// Notes this CTA's job for the join.  One thread.
+__device__ __forceinline__ void note_job(const AttendParams& p, int R, const int* prefix, const Share& sh) {
   JoinJob j = {};
   j.last = -1;
-  if (start < end) {
-    const int t = tile_of(p, prefix, end - 1), tu = prefix[t + 1] - prefix[t];
-    int64_t u0 = static_cast<int64_t>(prefix[t]) * p.c.heads;
-    int h = 0;
-    while (u0 + tu < end) u0 += tu, ++h;  // (a head at a time: no division, which would be a function)
-    if (u0 + tu > end && u0 >= start) {
+  if (sh.start < sh.end) {
+    const int t = tile_of(p, prefix, sh.heads, sh.end - 1), tu = prefix[t + 1] - prefix[t];
+    int64_t u0 = static_cast<int64_t>(prefix[t]) * sh.heads;
+    int h = sh.h;
+    while (u0 + tu < sh.end) u0 += tu, ++h;  // (a head at a time: no division, which would be a function)
+    if (u0 + tu > sh.end && u0 >= sh.start) {
       const Tile x = tile_at(p, t, R);
-      j = JoinJob{u0 + tu - 1, units, static_cast<int>(2 * blockIdx.x) + (u0 == start ? 0 : 1), x.rows, x.q0, x.first, h};
+      j = JoinJob{u0 + tu - 1, sh.units, static_cast<int>(2 * blockIdx.x) + (u0 == sh.start ? 0 : 1), x.rows, x.q0, x.first, h};
     }
   }
   p.jobs[blockIdx.x] = j;

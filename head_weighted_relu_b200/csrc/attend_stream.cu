@@ -460,14 +460,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
   __shared__ int prefix[kMaxSplitTiles + 1];
   __shared__ int warp_sums[kWarps];
   const int total = tile_prefix<kUnit, kWarps * 32>(p, R, prefix, warp_sums);
-  const int64_t units = static_cast<int64_t>(total) * p.c.heads;
-  const int64_t n = min(units, static_cast<int64_t>(p.n_ctas));
-  int64_t u = 0, end = 0;
-  if (blockIdx.x < n) u = share_start(blockIdx.x, units, n), end = share_start(blockIdx.x + 1, units, n);
-  if (threadIdx.x == 0) note_job(p, R, prefix, units, u, end);
+  const Share sh = share_of(p, total);
+  int64_t u = sh.start;
+  const int64_t end = sh.end;
+  if (threadIdx.x == 0) note_job(p, R, prefix, sh);
   bool first = true;
   while (u < end) {
-    const Piece g = piece_at(p, prefix, u, end);
+    const Piece g = piece_at(p, prefix, sh, u, end);
     segment<D, NT, F16>(p, tile_at(p, g.tile, R), g.h, g.u0, g.u1, g.whole,
                         2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1), smem);
     first = false;
@@ -482,7 +481,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm<D, NT>)
 template <int D>
 __device__ __forceinline__ void add_parts(const AttendParams& p, int first, int parts, int R, int i, int c, int step,
                                           int d, float& m, float& l, float (&o)[D / 32]) {
-  auto index = [&](int k) { return (k == 0 ? first : 2 * (static_cast<int64_t>(blockIdx.x) + k)) * R + i; };
+  auto index = [&](int k) { return (k == 0 ? first : 2 * (static_cast<int64_t>(blockIdx.x) + k * p.lanes)) * R + i; };
   m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
@@ -513,8 +512,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinJob g = p.jobs[blockIdx.x];
   if (g.last < 0) return;
-  const int parts = static_cast<int>(share_owner(g.last, g.units, min(g.units, static_cast<int64_t>(p.n_ctas)))) -
-                    static_cast<int>(blockIdx.x) + 1;
+  const int parts = static_cast<int>(share_owner(g.last, g.units, min(g.units, static_cast<int64_t>(p.n_ctas / p.lanes)))) -
+                    static_cast<int>(blockIdx.x / p.lanes) + 1;
   constexpr int kN = D / 32, kWarps = 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d = lane * kN;
   const bool together = parts > kWarps;

@@ -818,25 +818,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   // The CTA's share of the units, or its one (tile, head): where it starts, and
   // its units.
   int tile, h, u0;
-  int64_t share, start = 0, all = 0;
+  Share sh = {};
   if (p.n_ctas) {
-    const int total = tile_prefix<kKeys, kThreads>(p, R, prefix, prefix + kMaxSplitTiles2 + 1);
-    const int64_t units = static_cast<int64_t>(total) * p.c.heads, n = min(units, static_cast<int64_t>(p.n_ctas));
-    if (blockIdx.x >= n) {
-      if (threadIdx.x == 0) note_job(p, R, prefix, units, 0, 0);
+    sh = share_of(p, tile_prefix<kKeys, kThreads>(p, R, prefix, prefix + kMaxSplitTiles2 + 1));
+    if (sh.start == sh.end) {
+      if (threadIdx.x == 0) note_job(p, R, prefix, sh);
       return;
     }
-    const int64_t u = share_start(blockIdx.x, units, n), end = share_start(blockIdx.x + 1, units, n);
-    const Piece c = piece_at(p, prefix, u, end);
-    tile = c.tile, h = c.h, u0 = c.u0, share = end - u;
-    start = u, all = units;
+    const Piece c = piece_at(p, prefix, sh, sh.start, sh.end);
+    tile = c.tile, h = c.h, u0 = c.u0;
   } else {
     tile = p.n_tiles - 1 - blockIdx.x / p.c.heads;  // those of a sequence that see most, first
     h = blockIdx.x % p.c.heads, u0 = 0;
     const Tile x = tile_at(p, tile, R);
     if (x.rows <= 0) return;
-    share = tile_units<kKeys>(x);
-    if (threadIdx.x == 0) prefix[tile & 1] = 0, prefix[(tile & 1) + 1] = static_cast<int>(share);
+    sh.end = tile_units<kKeys>(x), sh.heads = p.c.heads;
+    if (threadIdx.x == 0) prefix[tile & 1] = 0, prefix[(tile & 1) + 1] = static_cast<int>(sh.end);
     prefix += (tile & 1) - tile;  // prefix[tile], prefix[tile + 1]
   }
   if (warp == 16) {
@@ -875,13 +872,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   const int tile_first = tile, h_first = h, u_first = u0;
   auto each = [&](bool with_tile, auto&& role) {
     uint32_t tiles = 0, segs = 0;
-    int64_t left = share;
+    int64_t left = sh.end - sh.start;
     int t = tile_first, hh = h_first, at = u_first;
     while (left > 0) {
       const int units = prefix[t + 1] - prefix[t];
       if (at >= units) {  // the next head, or tile
         at = 0;
-        if (units == 0 || ++hh == p.c.heads) ++t, hh = 0;
+        if (units == 0 || ++hh == sh.h + sh.heads) ++t, hh = sh.h;
         continue;
       }
       Segment g;
@@ -914,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
   regs_to<Regs<NM>::kIssue>();
   if (warp != 16) {
     each(true, [&](const Segment& g, uint32_t tiles, uint32_t) { look_up<D, NM, U16>(p, g, smem, tiles); });
-    if (warp == 17 && lane == 0 && p.n_ctas) note_job(p, R, prefix, all, start, start + share);
+    if (warp == 17 && lane == 0 && p.n_ctas) note_job(p, R, prefix, sh);
     return;
   }
   const uint32_t one = elect_lane();
