@@ -19,11 +19,13 @@
 // interleaved by byte permutes.  The weights pass to the second product
 // through a register transpose (movmatrix).
 //
-// What bounds it: reading the keys and values, in the end.  16 sequences of
-// 16,384 to 65,536 tokens, 8 heads: 256 us for 1.34 GB, 5.3 TB/s, 80% of what a
-// copy reaches; the integer pipe (code conversions, permutes, translation) is
-// busy 52% of the time and the issue slots 56%.  1,024 rows over 2,048 selected
-// tokens each of 16,384 (the cache in L2): 578 us, 7.4 TB/s out of L2.
+// What bounds it: reading the keys and values.  16 sequences of 16,384 to 65,536
+// tokens, 8 heads: 216 us for 1.34 GB, 6.2 TB/s, 95% of what a copy reaches.  That
+// took the heads of a token to be read side by side (CTAs c, c + 1, .. on the same
+// keys): a head alone is 128 bytes of every 1,024, 258 us.  One entry for 16
+// tokens that share their scales, instead of one each, changed nothing.  1,024
+// rows over 2,048 selected tokens each of 16,384 (the cache in L2): 578 us, 7.4
+// TB/s out of L2.
 #include "attend.cuh"
 
 namespace hwr {

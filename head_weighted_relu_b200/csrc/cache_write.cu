@@ -9,7 +9,7 @@
 // lane needs another's values), elsewhere eight in a row.
 //
 // Measured: FP8 rows of 16,384 tokens x 64 heads x 128, 64 dimensions rotated:
-// 100 us for 411 MB, 4.1 TB/s; the integer pipe is busy 67% of the time (16-bit
+// 100 us for 407 MB, 4.1 TB/s; the integer pipe is busy 67% of the time (16-bit
 // values unpacked, row maxima, codes packed: half-rate instructions), the issue
 // slots 70%.  The append of 8,192 tokens (64 heads of q, 8 of k and v): q 42 us
 // for 268 MB, 6.4 TB/s, as a copy; keys and values 25 us for 50 MB, bound by
@@ -111,12 +111,12 @@ __device__ __forceinline__ uint2 pack_codes(const float (&y)[8]) {
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __restrict__ x, int64_t S, int H,
                                                               int64_t x_stride, const int32_t* __restrict__ positions,
-                                                              RotView rot, int heads_per, uint8_t* __restrict__ codes,
+                                                              RotView rot, int parts, int heads_per, uint8_t* __restrict__ codes,
                                                               float* __restrict__ scale, uint32_t* status) {
   const int lane = threadIdx.x & 31, sub = lane % kLanes<D>;
-  const int64_t t = (blockIdx.x * int64_t(8) + (threadIdx.x >> 5)) * kRows<D> + lane / kLanes<D>;
+  const int64_t t = (blockIdx.x / parts * int64_t(8) + (threadIdx.x >> 5)) * kRows<D> + lane / kLanes<D>;
   const bool live = t < S;
-  const int h0 = blockIdx.y * heads_per, h1 = min(H, h0 + heads_per);
+  const int h0 = blockIdx.x % parts * heads_per, h1 = min(H, h0 + heads_per);
   Angles a;
   bool ok = live;
   if (rot.rot && live) {
@@ -199,8 +199,9 @@ constexpr int kAppendCtas = 2;  // of an SM
 template <int D, bool F16, int U>
 __device__ __forceinline__ void rotate_q(const AppendParams& p, int i) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes<D>, rsub = lane / kLanes<D>;
-  const int r = (i % p.q_slots * kAppendWarps + warp) * kRows<D> + rsub;
-  const int h0 = i / p.q_slots * p.q_heads, h1 = min(p.Hq, h0 + p.q_heads);
+  const int parts = (p.Hq + p.q_heads - 1) / p.q_heads;  // of a row, side by side
+  const int r = (i / parts * kAppendWarps + warp) * kRows<D> + rsub;
+  const int h0 = i % parts * p.q_heads, h1 = min(p.Hq, h0 + p.q_heads);
   Angles a;
   bool ok = r < p.s.S && r < seq_row(p.s, p.s.B);
   if (ok) {
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) cache_append_k
     return;
   }
 
-  const int slot = blockIdx.x % p.kv_slots, part = blockIdx.x / p.kv_slots;
+  const int slot = blockIdx.x / p.kv_split, part = blockIdx.x % p.kv_split;
   const int blk = p.c.block;
   const int b = slot_owner(p.s, slot, 1, blk, 2);
   const int row0 = seq_row(p.s, b), row1 = seq_row(p.s, b + 1);
@@ -386,10 +387,11 @@ cudaError_t launch_rotate_quantise(const void* x, int64_t S, int H, int D, bool 
   int split = 1;
   while (bx * split < 16 * sms && split * 8 <= H) split *= 2;
   const int per = (H + split - 1) / split;
-  const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>((H + per - 1) / per));
+  const int parts = (H + per - 1) / per;  // of a row, side by side
+  const unsigned grid = static_cast<unsigned>(bx * parts);
   const uint8_t* xb = static_cast<const uint8_t*>(x);
 #define HWR_GO(DD, FF)                                                                                            \
-  rotate_quantise_kernel<DD, FF><<<grid, 256, 0, stream>>>(xb, S, H, x_stride * 2, positions, rot, per, codes,    \
+  rotate_quantise_kernel<DD, FF><<<grid, 256, 0, stream>>>(xb, S, H, x_stride * 2, positions, rot, parts, per, codes,    \
                                                            scale, status)
   if (D == 128) {
     if (f16) HWR_GO(128, true); else HWR_GO(128, false);
