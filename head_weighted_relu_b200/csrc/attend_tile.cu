@@ -297,7 +297,6 @@ __device__ __forceinline__ void take_nans(uint4 (&r)[D / 16], uint8_t* nan, uint
 template <int D, int NM, bool U16>
 __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, uint8_t* smem, uint32_t tiles) {
   using L = Lay<D, NM, U16>;
-  constexpr int kAhead = 1;  // tiles whose codes are on the way
   Bars* bars = reinterpret_cast<Bars*>(smem + L::kBars);
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, ch = lane % (D / 16);
   const bool is_v = threadIdx.x >> 7 & 1;
@@ -310,36 +309,30 @@ __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, ui
   uint64_t* empty = is_v ? bars->vempty : bars->kempty;
   uint64_t* full = is_v ? bars->vfull : bars->kfull;
   const int n = g.n;
-  uint4 c[kAhead][D / 16];
-  auto load = [&](int j, uint4(&r)[D / 16]) {
+  uint4 c[D / 16];  // codes of the tile ahead
+  auto load = [&](int j) {
     if (j >= n) return;
     const uint32_t slot = (tiles + j) % L::kRing;
     wait(bars, &bars->tfull[slot], (tiles + j) / L::kRing & 1);
-    load_codes<D, U16>(base, row16, reinterpret_cast<const uint2*>(smem + L::kPlace) + slot * L::kEntries, r);
+    load_codes<D, U16>(base, row16, reinterpret_cast<const uint2*>(smem + L::kPlace) + slot * L::kEntries, c);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->tempty[slot]);
   };
-#pragma unroll
-  for (int a = 0; a < kAhead; ++a) load(a, c[a]);
+  load(0);
 #pragma unroll 1
-  for (int j0 = 0; j0 < n; j0 += kAhead) {
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int j = j0 + a;
-      if (j >= n) break;
-      const uint32_t t = tiles + j, slot = t & 1;
-      wait(bars, &empty[slot], (t >> 1 & 1) ^ 1);
-      // Tokens that some rows see and others do not: a NaN among their values
-      // must not reach the latter as 0 * NaN, so it is noted beside the tile.
-      if ((j + 1) * kKeys > partial)
-        take_nans<D>(c[a], smem + L::kNan + slot * (128 * 16),
-                     reinterpret_cast<uint32_t*>(smem + L::kNanAny) + slot * 4 + warp);
-      store_codes<D>(dst + slot * L::kKV, c[a]);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[slot]);
-      load(j + kAhead, c[a]);
-    }
+  for (int j = 0; j < n; ++j) {
+    const uint32_t t = tiles + j, slot = t & 1;
+    wait(bars, &empty[slot], (t >> 1 & 1) ^ 1);
+    // Tokens that some rows see and others do not: a NaN among their values must
+    // not reach the latter as 0 * NaN, so it is noted beside the tile.
+    if ((j + 1) * kKeys > partial)
+      take_nans<D>(c, smem + L::kNan + slot * (128 * 16),
+                   reinterpret_cast<uint32_t*>(smem + L::kNanAny) + slot * 4 + warp);
+    store_codes<D>(dst + slot * L::kKV, c);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[slot]);
+    load(j + 1);
   }
 }
 
