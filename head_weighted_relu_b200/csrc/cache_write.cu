@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __r
       if (!ok || !(m < INFINITY)) m = NAN;  // the whole row becomes NaN codes
       // scale = m / 448 and code = RNE_e4m3(y / scale), both quotients rounded to
       // nearest by a residual step (Markstein, 1990): with r the correctly rounded
-      // reciprocal of b and q = a r, the quotient is q + r (a - q b), unless b's
+      // reciprocal of b and q = a r, the quotient is q - r (q b - a), unless b's
       // fraction is all ones or something leaves the normal range.  Such rows
       // take the division itself.
       constexpr float k448 = 1.f / 448.f;
@@ -156,8 +156,10 @@ __global__ void __launch_bounds__(256) rotate_quantise_kernel(const uint8_t* __r
         const float inv = __frcp_rn(sc);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-          const float2 v = make_float2(y[i], y[i + 1]), r2 = make_float2(inv, inv);
-          const float2 q = mul2(v, r2), w = fma2(fma2(q, make_float2(-sc, -sc), v), r2, q);
+          // (q b - a, not a - q b: an exact quotient then keeps the sign of a zero)
+          const float2 q = mul2(make_float2(y[i], y[i + 1]), make_float2(inv, inv));
+          const float2 r = make_float2(fmaf(q.x, sc, -y[i]), fmaf(q.y, sc, -y[i + 1]));
+          const float2 w = fma2(r, make_float2(-inv, -inv), q);
           z[i] = w.x, z[i + 1] = w.y;
         }
       } else {

@@ -100,6 +100,28 @@ def test_rotation_rounds_each_product_on_its_own(cuda_ok, act, D, rot, inter):
     assert torch.equal(codes.cpu(), (y / want[..., None]).to(torch.float8_e4m3fn).view(torch.uint8))
 
 
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+def test_rotate_quantise_over_the_whole_range(cuda_ok, act):
+    """Rows of every magnitude that the type holds, subnormal scales among them, and
+    values from the row's largest down to nothing: scale and codes as IEEE division
+    gives them."""
+    I = _I()
+    g = torch.Generator().manual_seed(8)
+    lo, hi = (-133, 127) if act == "bf16" else (-24, 15)
+    mag = 2.0 ** torch.arange(lo, hi, dtype=torch.float64)
+    rows = torch.rand(len(mag), 3, 128, generator=g, dtype=torch.float64) * 2 - 1
+    rows *= 2.0 ** -(torch.arange(128) % 24)                      # down to below the least code
+    rows[:, 1, 5] = 1.9921875                                     # the largest fraction of 8 bits
+    x = (rows * mag[:, None, None]).to(ACT[act])
+    codes, scale = I.rotate_quantise(x.cuda())
+    xf = x.float()
+    amax = xf.abs().amax(-1)
+    want = torch.where(amax > 0, amax / 448, torch.ones_like(amax))
+    assert torch.equal(scale.cpu(), want)
+    z = (xf / want[..., None]).clamp(-448, 448)                   # (a subnormal scale is coarse: past 448 by its rounding)
+    assert torch.equal(codes.cpu(), z.to(torch.float8_e4m3fn).view(torch.uint8))
+
+
 def test_append_of_many_rows(cuda_ok):
     """Large enough for q to go through a kernel of its own: the same rows as in
     pieces, and the cache with them."""
