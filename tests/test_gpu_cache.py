@@ -586,6 +586,34 @@ def test_attend_calls_at_once_and_rows_on_their_own(cuda_ok, kernel):
     assert torch.equal(out[[1, 3]], want[0][[1, 3]])
 
 
+def test_pages_beyond_32_bits(cuda_ok):
+    """Pages 128 MB apart, most of them past 4 GB: the same cache, append and
+    attention as with the pages side by side."""
+    I = _I()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    pages, page, heads, D, n, gap = 48, 64, 2, 128, 48 * 64 - 5, 1 << 27
+    far = [torch.empty(pages * gap, dtype=torch.uint8, device="cuda").as_strided((pages, page, heads, D),
+                                                                                 (gap, heads * D, D, 1)) for _ in range(2)]
+    near = I.allocate_cache(pages, page, heads, D, 16)
+    wide = I.KVCache(*far, torch.empty_like(near.k_scale), torch.empty_like(near.v_scale))
+    table = torch.randperm(pages, generator=g, device="cuda").int().view(1, pages)
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    k, v = (torch.randn(n, heads, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    rt = I.rope_table(n, 128)
+    for c in (near, wide):
+        I.cache_append(c, k[:-1], v[:-1], ints(0, n - 1), ints(n - 1), table, table=rt)
+        I.cache_append(c, k[-1:], v[-1:], ints(0, 1), ints(n), table, table=rt)
+    used = (torch.arange(pages * page, device="cuda") < n).view(pages, page)
+    order = table[0].long()
+    for a, b in ((near.k, wide.k), (near.v, wide.v)):
+        assert torch.equal(a[order][used], b[order][used])
+    q = torch.randn(3, 24 * heads, D, generator=g, device="cuda").bfloat16()
+    sel = (torch.arange(0, n - 3, 7, device="cuda").int().repeat(3, 1), ints(300, 100, 437))
+    for kw in (dict(kernel=STREAM), dict(kernel=TILE), dict(selected=sel, kernel=STREAM), dict(selected=sel, kernel=TILE)):
+        one, two = (I.cache_attend(c, q, ints(0, 3), ints(n), table, **kw) for c in (near, wide))
+        assert torch.equal(one, two) and one.isfinite().all()
+
+
 def test_attend_in_large_prefill(cuda_ok):
     """More tiles than CTAs share: against the same rows in pieces."""
     I = _I()
