@@ -54,6 +54,7 @@ struct AttendParams {
   float* part_o;           // [2 n_ctas][rows][D]
   float2* part_ml;         // [2 n_ctas][rows]: reference and sum
   uint32_t* status;
+  int32_t test_wait;       // test hook: the tile kernel's look-ups do not come
 };
 
 // A tile: up to R consecutive rows of one sequence's (query, head in group)

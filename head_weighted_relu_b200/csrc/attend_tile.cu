@@ -73,7 +73,7 @@ struct Bars {
   uint64_t qfull, ofull, done, left;
   uint64_t tfull[8], tempty[8];
   uint32_t tmem;
-  int abort;
+  int abort, tries;  // a wait has run out; suspended tries until it does
 };
 
 // Dynamic shared memory, from a 1,024-byte boundary.
@@ -132,11 +132,23 @@ __device__ __forceinline__ uint32_t cvt_hi(uint32_t w) { return e4m3x2_to_f16x2(
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
 
 // A wait that, once it has run out, makes every further wait of the CTA end at
-// once: the loops then run through on whatever the buffers hold, all within
-// bounds, and the rows become NaN.  A try suspends the thread for up to
-// kTryNs, so that waiting warps take no issue slots from the others.
+// once: the loops then run through on what the buffers hold, all within bounds
+// (nothing is loaded from a place that no look-up gave), and the rows become NaN.
+// A try suspends the thread for up to kTryNs, so that waiting warps take no
+// issue slots from the others.
 constexpr uint32_t kTryNs = 100000;
-constexpr int kWaitTries = 100000;
+constexpr int kWaitTries = 100000, kTestTries = 10;
+__device__ __forceinline__ bool try_now(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool try_long(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -148,13 +160,14 @@ __device__ __forceinline__ bool try_long(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ void wait(Bars* b, uint64_t* bar, uint32_t parity) {
+// False when it ran out.
+__device__ __forceinline__ bool wait(Bars* b, uint64_t* bar, uint32_t parity) {
+  if (try_now(bar, parity)) return true;
 #pragma unroll 1
-  for (int i = 0; !try_long(bar, parity); ++i)
-    if (i >= kWaitTries || *reinterpret_cast<volatile int*>(&b->abort)) {
-      *reinterpret_cast<volatile int*>(&b->abort) = 1;
-      return;
-    }
+  for (int i = 0; i < *reinterpret_cast<volatile int*>(&b->tries) && !*reinterpret_cast<volatile int*>(&b->abort); ++i)
+    if (try_long(bar, parity)) return true;
+  *reinterpret_cast<volatile int*>(&b->abort) = 1;
+  return false;
 }
 
 // What a segment is: keys [128 u0, 128 u1) of (tile, head).
@@ -181,6 +194,7 @@ __device__ __forceinline__ void look_up(const AttendParams& p, const Segment& g,
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 17;
   const int end = min(g.x.n_keys, (g.u0 + g.n) * kKeys);
   const Translate tr(p, g.x, g.h, end);
+  if (p.test_wait) return;  // (test hook: looks up nothing, so that the others' waits run out)
 #pragma unroll 1
   for (int j0 = 0; j0 < g.n; j0 += 3 * kTiles) {
     const int j = j0 + warp * kTiles + (U16 ? lane >> 3 & 1 : 0), en = U16 ? lane & 7 : lane;
@@ -229,8 +243,9 @@ __device__ __forceinline__ void look_up(const AttendParams& p, const Segment& g,
 
 // ------------------------------------------------------------------- fill --
 // Four warps fill the keys' tiles and four the values', 32 tokens of each a warp.
+// on: `place` holds a look-up; otherwise nothing is loaded.
 template <int D, bool U16>
-__device__ __forceinline__ void load_codes(const uint8_t* base, uint32_t row16, const uint2* place,
+__device__ __forceinline__ void load_codes(const uint8_t* base, uint32_t row16, const uint2* place, bool on,
                                            uint4 (&r)[D / 16]) {
   constexpr int kCh = D / 16, kRowsPer = 32 / kCh;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
@@ -243,7 +258,7 @@ __device__ __forceinline__ void load_codes(const uint8_t* base, uint32_t row16, 
     for (int i = 0; i < kCh / 2; ++i) {
       const uint32_t t = i * kRowsPer + lane / kCh;
       if (!U16) w = place[warp * 32 + g * 16 + t], at = base + (static_cast<int64_t>(w.x) << 4);
-      r[g * (kCh / 2) + i] = (U16 ? t : 0u) < w.y
+      r[g * (kCh / 2) + i] = on && (U16 ? t : 0u) < w.y
                                  ? ldg_stream(U16 ? at + static_cast<int64_t>(i * kRowsPer * 16) * row16 : at)
                                  : make_uint4(0, 0, 0, 0);
     }
@@ -313,8 +328,8 @@ __device__ __forceinline__ void fill(const AttendParams& p, const Segment& g, ui
   auto load = [&](int j) {
     if (j >= n) return;
     const uint32_t slot = (tiles + j) % L::kRing;
-    wait(bars, &bars->tfull[slot], (tiles + j) / L::kRing & 1);
-    load_codes<D, U16>(base, row16, reinterpret_cast<const uint2*>(smem + L::kPlace) + slot * L::kEntries, c);
+    const bool on = wait(bars, &bars->tfull[slot], (tiles + j) / L::kRing & 1);
+    load_codes<D, U16>(base, row16, reinterpret_cast<const uint2*>(smem + L::kPlace) + slot * L::kEntries, on, c);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->tempty[slot]);
   };
@@ -849,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const __grid_c
       mbar_init(&bars->ofull, 1);
       mbar_init(&bars->done, 1);
       mbar_init(&bars->left, kSoftThreads / 32);
-      bars->abort = 0;
+      bars->abort = 0, bars->tries = p.test_wait ? kTestTries : kWaitTries;
       fence_mbar_init();
     }
     __syncwarp();

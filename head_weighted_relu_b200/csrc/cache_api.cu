@@ -89,9 +89,11 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   st = view_seqs(s, pointers, &p.s);
   if (st != INDEXER_OK) return st;
   if (!a || !act_ok(a->act) || a->Hq < 1 || a->Hq % c->heads != 0 || a->sel_width < 0 || a->max_q < 0 ||
-      (a->causal != 0 && a->causal != 1) || !isfinite(a->scale) || a->kernel < INDEXER_ATTEND_AUTO ||
-      a->kernel > INDEXER_ATTEND_TILE)
+      (a->causal != 0 && a->causal != 1) || !isfinite(a->scale))
     return INDEXER_EINVAL;
+  p.test_wait = a->kernel == (INDEXER_ATTEND_TILE | INDEXER_ATTEND_TEST_WAIT_TIMEOUT);
+  const int32_t kernel = p.test_wait ? INDEXER_ATTEND_TILE : a->kernel;
+  if (kernel < INDEXER_ATTEND_AUTO || kernel > INDEXER_ATTEND_TILE) return INDEXER_EINVAL;
   p.Hq = a->Hq;
   p.G = a->Hq / c->heads;
   if (p.G > 128) return INDEXER_EUNSUPPORTED;
@@ -116,8 +118,8 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   // us, one query of 64 heads over 1M tokens 258 and 115 us.
   const double units = static_cast<double>(a->sel_width ? s->S : s->B) * c->heads * most_keys / 128 / sms;
   const int64_t passes = (most_rows + 15) / 16;
-  const bool tile = a->kernel == INDEXER_ATTEND_TILE ||
-                    (a->kernel == INDEXER_ATTEND_AUTO && passes > 2 && units * (0.9 * passes - 1.7) > 30);
+  const bool tile = kernel == INDEXER_ATTEND_TILE ||
+                    (kernel == INDEXER_ATTEND_AUTO && passes > 2 && units * (0.9 * passes - 1.7) > 30);
   const int R = pl->rows = tile ? (most_rows <= 128 ? 128 : 256) : (most_rows <= 8 ? 8 : 16);
   p.sel_tiles = (p.G + R - 1) / R;
   const int64_t tiles = a->sel_width ? s->S * p.sel_tiles : s->S * p.G / R + s->B;

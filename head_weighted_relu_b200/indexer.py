@@ -65,6 +65,7 @@ class Problem(ctypes.Structure):
 
 ACT_BF16, ACT_FP16 = 0, 1
 ATTEND_AUTO, ATTEND_STREAM, ATTEND_TILE = 0, 1, 2   # kernels of cache_attend
+ATTEND_TEST_WAIT_TIMEOUT = 1 << 8   # with ATTEND_TILE: test hook of its failure path
 STATUS_TOKEN = 8   # status bit of the cache calls: a token's page or position does not exist
 
 

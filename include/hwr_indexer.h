@@ -496,6 +496,14 @@ typedef enum {
   INDEXER_ATTEND_TILE = 2
 } indexer_attend_kernel;
 
+/* Test hook for the tile kernel's failure path (not for production use): as
+ * INDEXER_ATTEND_TILE | INDEXER_ATTEND_TEST_WAIT_TIMEOUT, the warps that look
+ * up the keys' places give none, and the waits for them run out after about a
+ * millisecond.  Every role then runs through without loading a key or value,
+ * all rows become NaN, and bit 0 of *status is set; the device stays usable
+ * for the next call. */
+enum { INDEXER_ATTEND_TEST_WAIT_TIMEOUT = 1 << 8 };
+
 /* Workspace of indexer_cache_attend: scratch between calls, no
  * initialisation; calls that may overlap on the GPU need one each. */
 indexer_status indexer_cache_attend_workspace_bytes(const indexer_cache* cache, const indexer_sequences* seqs,
