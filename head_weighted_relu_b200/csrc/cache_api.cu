@@ -53,6 +53,8 @@ indexer_status view_cache(const indexer_cache* c, CacheView* v) {
   if (c->n_pages > 1 && c->page_stride < c->D) return INDEXER_EINVAL;
   if (inner == INT64_MAX) return INDEXER_EINVAL;
   if (c->page_stride > (int64_t(1) << 36) / c->n_pages || inner > (int64_t(1) << 36)) return INDEXER_EUNSUPPORTED;
+  // the attention holds a token's offset in 32 bits, in units of 16 bytes
+  if ((c->n_pages - 1) * c->page_stride + tok_span >= int64_t(1) << 36) return INDEXER_EUNSUPPORTED;
   if (c->n_pages > INT32_MAX) return INDEXER_EUNSUPPORTED;
   int shift = 0;
   while ((1 << shift) < c->block) ++shift;

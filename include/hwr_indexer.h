@@ -408,7 +408,8 @@ typedef struct {
   float* k_scale;
   float* v_scale;
   int64_t n_pages;
-  int64_t page_stride;   /* bytes; n_pages * page_stride at most 2^36 */
+  int64_t page_stride;   /* bytes; n_pages * page_stride, and a page's extent, at most
+                            2^36, and every token begins below 2^36 */
   int64_t token_stride;
   int64_t head_stride;
   int32_t page_size;     /* tokens a page, a multiple of block, at most 2^20 */

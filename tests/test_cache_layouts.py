@@ -1,0 +1,42 @@
+"""Which cache layouts the calls take (no GPU needed: a refused call launches
+nothing, and without a device an accepted one stops before its launch)."""
+
+import pytest
+import torch
+
+from tests.test_cache_arguments import ECUDA, EINVAL, EUNSUPPORTED, I, _append, _attend, _cache  # noqa: F401
+
+GB = 1 << 30
+
+
+def _token_major(tokens, pages, heads=8, D=128):
+    """Pages interleaved by token: [tokens of a page, pages, heads, D]."""
+    return dict(n_pages=pages, page_size=tokens, page_stride=heads * D, token_stride=pages * heads * D,
+                head_stride=D, heads=heads, D=D)
+
+
+def _both(I, layout):  # noqa: F811
+    return _append(I, cache=_cache(I, **layout)), _attend(I, cache=_cache(I, **layout))
+
+
+@pytest.mark.parametrize("layout", [
+    _token_major(64, 1 << 21),                                     # 128 GiB: tokens beyond 32 bits of 16 bytes
+    _token_major(64, 1 << 20) | dict(page_stride=2048, token_stride=1 << 31),
+    dict(n_pages=1 << 15, page_stride=1 << 21, page_size=16, token_stride=1 << 32),   # just over by the last page
+], ids=["128GiB", "gaps", "last-page"])
+def test_offsets_beyond_32_bits_are_refused(I, layout):  # noqa: F811
+    d = _cache(I, **layout)
+    last = (d.n_pages - 1) * d.page_stride + (d.page_size - 1) * d.token_stride
+    assert last >> 4 >= 1 << 32                                    # (what the kernels hold in 32 bits)
+    assert _both(I, layout) == (EUNSUPPORTED, EUNSUPPORTED)
+
+
+@pytest.mark.parametrize("layout", [
+    _token_major(64, 1 << 20),                                     # 64 GiB and no more
+    dict(n_pages=1 << 20, page_stride=1 << 16),                    # the same, page by page
+    dict(n_pages=1 << 20, page_stride=1 << 16, token_stride=128, head_stride=64 * 128),
+])
+def test_layouts_up_to_64_gib_are_taken(I, layout):  # noqa: F811
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: only where no GPU can follow them")
+    assert _both(I, layout) == (ECUDA, ECUDA)
