@@ -45,6 +45,9 @@ indexer_status view_cache(const indexer_cache* c, CacheView* v) {
   if (c->page_stride < 16 || c->token_stride < 16 || c->head_stride < c->D || c->page_stride % 16 != 0 ||
       c->token_stride % 16 != 0 || c->head_stride % 16 != 0)
     return INDEXER_EINVAL;
+  // (before any product of them)
+  if ((c->page_size > 1 && c->token_stride > int64_t(1) << 36) || (c->heads > 1 && c->head_stride > int64_t(1) << 36))
+    return INDEXER_EUNSUPPORTED;
   // two tokens or pages never share bytes
   const int64_t tok_span = (c->page_size - 1) * c->token_stride, head_span = (c->heads - 1) * c->head_stride + c->D;
   const int64_t inner = c->token_stride >= head_span

@@ -40,3 +40,15 @@ def test_layouts_up_to_64_gib_are_taken(I, layout):  # noqa: F811
     if torch.cuda.is_available():
         pytest.skip("made-up addresses: only where no GPU can follow them")
     assert _both(I, layout) == (ECUDA, ECUDA)
+
+
+@pytest.mark.parametrize("layout", [dict(token_stride=1 << 60), dict(head_stride=1 << 61), dict(token_stride=(1 << 62) + 1024),
+                                    dict(head_stride=1 << 60, heads=1024, token_stride=128), dict(page_stride=1 << 60)])
+def test_strides_whose_extent_overflows_are_refused(I, layout):  # noqa: F811
+    assert _both(I, layout) == (EUNSUPPORTED, EUNSUPPORTED)
+
+
+def test_strides_of_single_tokens_and_heads_do_not_count(I):  # noqa: F811
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: only where no GPU can follow them")
+    assert _both(I, dict(page_size=1, block=1, token_stride=1 << 60)) == (ECUDA, ECUDA)
