@@ -3,6 +3,8 @@
 // the caller's stream.  Nothing here allocates or synchronises.
 #include <math.h>
 
+#include <utility>
+
 #include "attend.cuh"
 #include "hwr_indexer.h"
 #include "internal.h"
@@ -48,13 +50,22 @@ indexer_status view_cache(const indexer_cache* c, CacheView* v) {
   // (before any product of them)
   if ((c->page_size > 1 && c->token_stride > int64_t(1) << 36) || (c->heads > 1 && c->head_stride > int64_t(1) << 36))
     return INDEXER_EUNSUPPORTED;
-  // two tokens or pages never share bytes
-  const int64_t tok_span = (c->page_size - 1) * c->token_stride, head_span = (c->heads - 1) * c->head_stride + c->D;
-  const int64_t inner = c->token_stride >= head_span
-                            ? tok_span + head_span
-                            : (c->head_stride >= tok_span + c->D ? tok_span + head_span : INT64_MAX);
-  if (c->n_pages > 1 && c->page_stride < c->D) return INDEXER_EINVAL;
-  if (inner == INT64_MAX) return INDEXER_EINVAL;
+  // No two rows of D codes share bytes: of pages, tokens and heads, in the order of
+  // their strides, each steps over all of the ones before.
+  struct {
+    int64_t n, stride;
+  } dim[3] = {{c->n_pages, c->page_stride}, {c->page_size, c->token_stride}, {c->heads, c->head_stride}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (dim[j].stride > dim[j + 1].stride) std::swap(dim[j], dim[j + 1]);
+  __int128 span = c->D;
+  for (const auto& d : dim) {
+    if (d.n == 1) continue;
+    if (d.stride < span) return INDEXER_EINVAL;
+    span += static_cast<__int128>(d.n - 1) * d.stride;
+  }
+  const int64_t tok_span = (c->page_size - 1) * c->token_stride;
+  const int64_t inner = tok_span + (c->heads - 1) * c->head_stride + c->D;
   if (c->page_stride > (int64_t(1) << 36) / c->n_pages || inner > (int64_t(1) << 36)) return INDEXER_EUNSUPPORTED;
   // the attention holds a token's offset in 32 bits, in units of 16 bytes
   if ((c->n_pages - 1) * c->page_stride + tok_span >= int64_t(1) << 36) return INDEXER_EUNSUPPORTED;

@@ -398,8 +398,9 @@ indexer_status indexer_rotate_quantise(const void* x, int64_t S, int32_t H, int3
 
 /* A paged cache of keys and values in e4m3 codes.  The token at offset o of
  * page p has its head h at byte p*page_stride + o*token_stride + h*head_stride
- * of k and of v (both have the same strides, multiples of 16; a head's D codes
- * are contiguous), and stands for code * scale with
+ * of k and of v (both have the same strides, multiples of 16, in any order of
+ * size; a head's D codes are contiguous, and no two heads, tokens or pages share
+ * bytes), and stands for code * scale with
  *   scale = k_scale[p, o / block, h]  (v_scale for values),
  * both [n_pages, page_size/block, heads] float32, positive and finite. */
 typedef struct {
