@@ -345,7 +345,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) cache_append_k
     else
       __syncwarp();
     uint8_t* dst = (is_v ? p.c.v : p.c.k) + (tok0 + h * p.c.head16 + tw * p.c.token16) * 16;
-    const float inv = __uint_as_float((254u << 23) - __float_as_uint(sc));  // 1 / sc: a power of two
+    // sc = frac * 2^e.  A block's own scales have frac = 1, and dividing by them is
+    // exact; a scale that another writer chose and that is kept may have any: then
+    // the quotient by frac, correctly rounded by a residual step as above.
+    const uint32_t bits = __float_as_uint(sc);
+    const float inv = bits < 254u << 23 ? __uint_as_float((254u << 23) - (bits & 0x7F800000u)) : 0x1p-127f;  // 2^-e
+    const bool pow2 = (bits & 0x7FFFFFu) == 0;
+    const float frac = __uint_as_float(bits & 0x7FFFFFu | 127u << 23), rfrac = __frcp_rn(frac);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       uint8_t* to = dst + i * kRows<D> * p.c.token16 * 16;
@@ -355,11 +361,18 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendCtas) cache_append_k
         if (on) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[i][e] *= inv;
+          if (!pow2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float q = y[i][e] * rfrac;
+              y[i][e] = fmaf(fmaf(q, frac, -y[i][e]), -rfrac, q);
+            }
+          }
           const uint2 code = pack_codes(y[i]);
           *lo4 = code.x, *hi4 = code.y;
         }
       } else if (on && tw + i * kRows<D> < lo && sc != old) {
-        // an earlier token of a block whose scale rises
+        // an earlier token of a block whose scale rises (to a power of two)
         const float f = old * inv;
         const uint32_t ww[2] = {*lo4, *hi4};
         float z[8];

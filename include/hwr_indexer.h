@@ -445,7 +445,8 @@ typedef struct {
  * powers of two keep every code's relative precision and make the change of
  * a block's scale exact except for codes that fall below 2^-6.  Where a
  * sequence's first new token lies inside a block, that block's earlier tokens
- * keep its scale as a lower bound; if it rises their codes become
+ * keep its scale, which another writer may have chosen and which then need not
+ * be a power of two, as a lower bound; if it rises their codes become
  * RNE_e4m3(code * old / new).  A block whose first token is new starts
  * anew, whatever it held.  Appending the same tokens again leaves the cache
  * as it is, and splitting an append at any token gives the same scales.

@@ -1,0 +1,63 @@
+"""Edges of the cache operators on the GPU: scales that are no power of two."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests import cache_reference as R
+from tests.test_gpu_cache import ACT, _dev, _half_step, _I, _random_cache, _snapshot
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------- append --
+
+@pytest.mark.parametrize("D,block,act,rot", [(128, 16, "bf16", 64), (64, 32, "fp16", 0), (128, 128, "bf16", 128),
+                                             (64, 128, "bf16", 0)])
+@pytest.mark.parametrize("old", ["1.5*2^-7", "0.3", "1.25", "amax/448", "2^127"])
+def test_append_behind_any_scale(cuda_ok, D, block, act, rot, old):
+    """A block begun by another writer, whose scale is no power of two (or too large
+    for its reciprocal to be a normal number): kept where the new tokens fit
+    under it, raised to a power of two where they do not."""
+    I = _I()
+    rng = np.random.default_rng(D + block)
+    heads, past, n = 3, 5, 9
+    cache = _random_cache(rng, 2, block, heads, D, block)
+    cache.k[1, :past] = _dev(R.to_code(np.clip(rng.normal(size=(past, heads, D)) * 100, -448, 448)))
+    cache.v[1, :past] = _dev(R.to_code(np.clip(rng.normal(size=(past, heads, D)) * 100, -448, 448)))
+    scale = {"1.5*2^-7": np.full(heads, 1.5 * 2.0 ** -7), "0.3": np.full(heads, 0.3), "1.25": np.full(heads, 1.25),
+             "amax/448": rng.uniform(1, 4, size=heads) / 448, "2^127": np.full(heads, 2.0 ** 127)}[old].astype(np.float32)
+    cache.k_scale[1, 0] = _dev(scale)
+    cache.v_scale[1, 0] = _dev(scale)
+    # the first head fits under the old scale, the last one may not
+    x = rng.normal(size=(n, heads, D)) * np.array([0.5, 3.0, 40.0])[:, None] * float(scale[0]) * 60
+    x = np.clip(x, -3e38, 3e38) if act == "bf16" else np.clip(x, -60000, 60000)
+    k, v = _dev(x, ACT[act]), _dev(-x[::-1], ACT[act])
+    before = _snapshot(cache)
+    rt = I.rope_table(64, rot) if rot else None
+    cu, kv = np.array([0, n], dtype=np.int32), [past + n]
+    table = np.array([[1]], dtype=np.int32)
+    I.cache_append(cache, k, v, _dev(cu), _dev(np.array(kv, dtype=np.int32)), _dev(table), table=rt)
+    after = _snapshot(cache)
+    wk, wv, wks, wvs, _, written = R.append(*before, R.to_np(k), R.to_np(v), cu, kv, table, rot, False)
+    for name, got, want, gs, ws, was, sc0 in (("k", after[0], wk, after[2], wks, before[0], before[2]),
+                                              ("v", after[1], wv, after[3], wvs, before[1], before[3])):
+        np.testing.assert_array_equal(gs[1], ws[1].astype(np.float32))
+        for (nm, pg, o, h), (y, s) in written.items():
+            if nm == name:
+                slip = 6 * 2.0 ** -24 * np.abs(R.to_np(k)[o - past, h]).max() if name == "k" and rot else 0.0
+                # (a rotation beyond FP32's range is infinite, and becomes NaN codes)
+                over = np.abs(y) >= 2.0 ** 128 * (1 - 2.0 ** -25)
+                assert ((got[pg, o, h] & 0x7F == 0x7F) == over).all()
+                y = np.where(over, 0.0, y)
+                err = np.where(over, 0.0, np.abs(R.VALUES[got[pg, o, h]] * s - y))
+                # rounded twice: the quotient, half a step of FP32, and the code
+                assert (err <= _half_step(y, s) * (1 + 2.0 ** -20) + slip).all(), (name, o, h)
+        for h in range(heads):
+            if ws[1, 0, h] == sc0[1, 0, h]:
+                np.testing.assert_array_equal(got[1, :past, h], was[1, :past, h])
+            else:
+                y, s = R.VALUES[was[1, :past, h]] * float(sc0[1, 0, h]), ws[1, 0, h]
+                assert (np.abs(R.VALUES[got[1, :past, h]] * s - y) <= _half_step(y, s) * (1 + 2.0 ** -20)).all()
+        np.testing.assert_array_equal(got[0], was[0])
+        np.testing.assert_array_equal(got[1, past + n:], was[1, past + n:])
