@@ -715,6 +715,9 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
   // Tiles of the segment that all of the warp's rows see whole.
   const int whole_tiles =
       p.sel_width ? g.n : (row_limit(p, g.x, g.x.first + min(r0 + first, g.x.rows - 1)) - g.u0 * kKeys) / kKeys;
+  // Tiles that all rows of the tile see whole: from here on fill() takes NaN codes
+  // out of the values, for the rows that do see them too.
+  const int clean_tiles = p.sel_width ? g.n : max(row_limit(p, g.x, g.x.first) - g.u0 * kKeys, 0) / kKeys;
   const uint32_t lanes = static_cast<uint32_t>(first) << 16, tm = bars->tmem + lanes;
   const uint32_t tm_s = tm + w * 128, tm_o = tm + 256 + w * 128;
   constexpr int kEvery = NM == 2 ? 1 : 2;
@@ -725,13 +728,14 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
     tc_fence_after();
     if (busy) {
       const float* sc = reinterpret_cast<const float*>(smem + L::kScale) + (tiles + j) % L::kRing * L::kScales;
-      const bool partial = j >= whole_tiles;
-      if (!partial) {
+      int see = kKeys;
+      if (j < whole_tiles) {
         softmax_tile<D, U16, false>(tm_s, tm_o, sc, row, kKeys, j < kEvery);
       } else {
-        const int see =
-            min(row_limit(p, g.x, g.x.first + min(r0 + t, g.x.rows - 1)) - (g.u0 + j) * kKeys, kKeys);
+        see = min(row_limit(p, g.x, g.x.first + min(r0 + t, g.x.rows - 1)) - (g.u0 + j) * kKeys, kKeys);
         softmax_tile<D, U16, true>(tm_s, tm_o, sc, row, see, j < kEvery);
+      }
+      if (j >= clean_tiles) {
         const uint32_t slot = (tiles + j) & 1;
         wait(bars, &bars->vfull[slot], (tiles + j) >> 1 & 1);
         const uint32_t* any = reinterpret_cast<const uint32_t*>(smem + L::kNanAny) + slot * 4;

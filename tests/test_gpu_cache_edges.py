@@ -1,13 +1,18 @@
-"""Edges of the cache operators on the GPU: scales that are no power of two."""
+"""Edges of the cache operators on the GPU: scales that are no power of two, NaN
+codes in tiles that only some rows see whole."""
 
 import numpy as np
 import pytest
 import torch
 
 from tests import cache_reference as R
-from tests.test_gpu_cache import ACT, _dev, _half_step, _I, _random_cache, _snapshot
+from tests.test_gpu_cache import ACT, STREAM, TILE, _check_attend, _dev, _filled, _half_step, _I, _random_cache, _snapshot
 
 pytestmark = pytest.mark.gpu
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
 # ----------------------------------------------------------------- append --
@@ -61,3 +66,28 @@ def test_append_behind_any_scale(cuda_ok, D, block, act, rot, old):
                 assert (np.abs(R.VALUES[got[1, :past, h]] * s - y) <= _half_step(y, s) * (1 + 2.0 ** -20)).all()
         np.testing.assert_array_equal(got[0], was[0])
         np.testing.assert_array_equal(got[1, past + n:], was[1, past + n:])
+
+
+# -------------------------------------------------------------- attention --
+
+@pytest.mark.parametrize("block", [16, 8])
+@pytest.mark.parametrize("G,n_q,kv,max_q,causal", [(8, 40, 140, 40, True), (1, 300, 420, 300, True), (8, 16, 134, 16, True),
+                                                   (3, 200, 700, 200, True), (8, 40, 140, 40, False)])
+def test_nan_value_in_a_tile_that_later_rows_see_whole(cuda_ok, G, n_q, kv, max_q, causal, block):
+    """Tiles of keys that a tile's first row sees in part and its last rows whole: a
+    NaN value code there reaches every row that sees it."""
+    I = _I()
+    rng = np.random.default_rng(G * 100 + n_q)
+    cache, table = _filled(rng, [kv], 2, 128, 32, block)
+    first = kv - n_q + 1                                   # positions that the first row sees
+    for p, d in ((50, 3), (first // 128 * 128, 77), (kv - 2, 100)):
+        cache.v[table[0, p // 32], p % 32, 1, d] = 0x7F
+    cu = np.array([0, n_q], dtype=np.int32)
+    q = _dev(rng.normal(size=(n_q, 2 * G, 128)), torch.bfloat16)
+    out = {}
+    for kernel in (TILE, STREAM):
+        out[kernel], lse = I.cache_attend(cache, q, _dev(cu), _ints([kv]), _dev(table), causal=causal, with_lse=True,
+                                          max_q=max_q, kernel=kernel)
+        _check_attend(cache, q, cu, [kv], table, 128 ** -0.5, causal, None, out[kernel], lse, "bf16")
+    nan = out[TILE].isnan()
+    assert torch.equal(nan, out[STREAM].isnan()) and nan[:, G:, 3].all() and not nan[:, :G].any()
