@@ -795,7 +795,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
     const float2 other = ml[t];
     const float m = fmaxf(row.m, other.x);
     const float f0 = row.m == -INFINITY ? 0.f : ex2(row.m - m), f1 = other.x == -INFINITY ? 0.f : ex2(other.x - m);
-    row.l = (f0 == 0.f ? 0.f : f0 * row.l) + (f1 == 0.f ? 0.f : f1 * other.y);
+    row.l = f0 * row.l + f1 * other.y;  // (NaN where either is, whatever the factors)
     row.m = m;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) row_nan[e] |= row_nan[128 * 4 + e];

@@ -1,5 +1,5 @@
 """Edges of the cache operators on the GPU: scales that are no power of two, NaN
-codes in tiles that only some rows see whole."""
+codes in tiles that only some rows see whole and beside large scores."""
 
 import numpy as np
 import pytest
@@ -91,3 +91,39 @@ def test_nan_value_in_a_tile_that_later_rows_see_whole(cuda_ok, G, n_q, kv, max_
         _check_attend(cache, q, cu, [kv], table, 128 ** -0.5, causal, None, out[kernel], lse, "bf16")
     nan = out[TILE].isnan()
     assert torch.equal(nan, out[STREAM].isnan()) and nan[:, G:, 3].all() and not nan[:, :G].any()
+
+
+def _ramp(rng, kv, heads, D, low):
+    """A cache whose keys score `low`[p] in every head against a query of ones."""
+    I = _I()
+    page = 64
+    pages = -(-kv // page)
+    table = rng.permutation(pages).astype(np.int32)[None]
+    cache = I.allocate_cache(pages, page, heads, D, 16)
+    code = R.to_code(low).astype(np.uint8)
+    flat = np.zeros((pages * page,), dtype=np.uint8)
+    flat[:kv] = code
+    by_page = np.empty((pages, page), dtype=np.uint8)
+    by_page[table[0]] = flat.reshape(pages, page)
+    cache.k.copy_(_dev(by_page)[:, :, None, None].expand(pages, page, heads, D))
+    cache.v.copy_(_dev(R.to_code(np.clip(rng.normal(size=(pages, page, heads, D)) * 60, -448, 448))))
+    cache.k_scale.fill_(2.0 ** -4)
+    cache.v_scale.fill_(2.0 ** -6)
+    return cache, table
+
+
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+@pytest.mark.parametrize("where", [5000, 5128])
+def test_nan_key_beside_large_scores(cuda_ok, kernel, where):
+    """Scores of some 200 (natural) everywhere, and a NaN code in one key, in an even
+    and in an odd tile: all rows that see it are NaN, whatever shares its sums."""
+    I = _I()
+    rng = np.random.default_rng(31)
+    kv, heads, D = 20000, 4, 128
+    cache, table = _ramp(rng, kv, heads, D, np.full(kv, 256.0))
+    cache.k[table[0, where // 64], where % 64, 1, 9] = 0x7F
+    q = torch.ones(1, heads * 8, D, dtype=torch.bfloat16, device="cuda")
+    out, lse = I.cache_attend(cache, q, _ints([0, 1]), _ints([kv]), _dev(table), scale=0.1, with_lse=True, max_q=1,
+                              kernel=kernel)
+    assert out[0, 8:16].isnan().all() and lse[0, 8:16].isnan().all()
+    assert out[0, :8].isfinite().all() and out[0, 16:].isfinite().all()
