@@ -220,7 +220,7 @@ __device__ __forceinline__ void store_rows(const AttendParams& p, const Tile& x,
       const float2 v = ml[w * R + i];
       const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
       l += f * v.y;
-      if (f != 0.f) {
+      if (v.x != -INFINITY) {  // (a part of a vanishing factor counts, for its NaN)
         const float* a = acc + (w * R + i) * (D + 4) + d;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += f * a[e];
@@ -505,7 +505,7 @@ __device__ __forceinline__ void add_parts(const AttendParams& p, int first, int 
     l += f * v.y;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e)
-      if (f != 0.f) o[e] += f * a[e];
+      if (v.x != -INFINITY) o[e] += f * a[e];
   }
 }
 
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
         l += f * v.y;
 #pragma unroll
         for (int e = 0; e < kN; ++e)
-          if (f != 0.f) o[e] += f * sum[k][d + e];
+          if (v.x != -INFINITY) o[e] += f * sum[k][d + e];
       }
     }
     const int pair = g.pair + i;

@@ -794,7 +794,10 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
   } else {
     const float2 other = ml[t];
     const float m = fmaxf(row.m, other.x);
-    const float f0 = row.m == -INFINITY ? 0.f : ex2(row.m - m), f1 = other.x == -INFINITY ? 0.f : ex2(other.x - m);
+    // (outputs of a stream that saw nothing may be anything; those of a vanishing
+    // factor count, for their NaN)
+    const bool on0 = row.m != -INFINITY, on1 = other.x != -INFINITY;
+    const float f0 = on0 ? ex2(row.m - m) : 0.f, f1 = on1 ? ex2(other.x - m) : 0.f;
     row.l = f0 * row.l + f1 * other.y;  // (NaN where either is, whatever the factors)
     row.m = m;
 #pragma unroll
@@ -810,7 +813,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
         const uint32_t b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[4 * e + k] = (f0 == 0.f ? 0.f : f0 * __uint_as_float(r[4 * e + k])) + (f1 == 0.f ? 0.f : f1 * __uint_as_float(b[k]));
+          o[4 * e + k] = (on0 ? f0 * __uint_as_float(r[4 * e + k]) : 0.f) + (on1 ? f1 * __uint_as_float(b[k]) : 0.f);
       }
       named_bar(kSoftBar, kSoftThreads);
     });

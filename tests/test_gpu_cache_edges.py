@@ -1,5 +1,6 @@
 """Edges of the cache operators on the GPU: scales that are no power of two, NaN
-codes in tiles that only some rows see whole and beside large scores."""
+codes in tiles that only some rows see whole, beside large scores and of vanishing
+weight."""
 
 import numpy as np
 import pytest
@@ -127,3 +128,22 @@ def test_nan_key_beside_large_scores(cuda_ok, kernel, where):
                               kernel=kernel)
     assert out[0, 8:16].isnan().all() and lse[0, 8:16].isnan().all()
     assert out[0, :8].isfinite().all() and out[0, 16:].isfinite().all()
+
+
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+@pytest.mark.parametrize("kv,every,part", [(20000, 20000, 10000), (20000, 64, 16), (20000, 256, 128), (600, 600, 300)])
+def test_nan_value_of_vanishing_weight(cuda_ok, kernel, kv, every, part):
+    """A NaN code among the values of keys that score hundreds less than the others,
+    by themselves in a warp's, a stream's or a CTA's share: 0 * NaN is NaN in
+    that dimension, and there alone."""
+    I = _I()
+    rng = np.random.default_rng(32)
+    heads, D = 2, 64
+    pos = np.arange(kv)
+    cache, table = _ramp(rng, kv, heads, D, np.where(pos % every < part, -256.0, 256.0))
+    for p in (min(3, part - 1), (kv - 1) // every * every):
+        cache.v[table[0, p // 64], p % 64, 1, 21] = 0xFF
+    q = torch.ones(1, heads * 8, D, dtype=torch.bfloat16, device="cuda")
+    out = I.cache_attend(cache, q, _ints([0, 1]), _ints([kv]), _dev(table), scale=0.2, max_q=1, kernel=kernel)
+    nan = out.isnan()
+    assert nan[0, 8:, 21].all() and nan.sum() == 8
