@@ -8,11 +8,15 @@
 // The value scale is a power of two (or any positive number) per token, so it
 // goes into the exponent: with u_j = t_j + log2 vs_j and a running reference
 // m >= max u_j - slack,
-//   acc = sum_j 2^{u_j - m + kHead} V_j,   l = sum_j 2^{u_j - m + kHead} / vs_j,
-//   o = acc / l,   log sum_j e^{...} = ln2 * (m - kHead + log2 l).
+//   acc = sum_j 2^{u_j - m + kHead} V_j,   l = sum_j 2^{u_j - m + kHead - kSum} / vs_j,
+//   o = 2^{-kSum} acc / l,   log sum_j e^{...} = ln2 * (m - kHead + kSum + log2 l).
 // The weights 2^{u_j - m + kHead} lie below 2^{kHead + slack} <= 2^15 and are
 // rounded to FP16 for the matrix instruction: 11 bits, and a weight vanishes
 // only below 2^{-25-kHead} of the largest.  V_j are the bare codes, exact in FP16.
+// The sum's terms span the value scales: a block of zeros has 2^-100, so that terms
+// reach 2^{15+100}, and a scale of 2^120 makes a row's largest 2^{7-120}.  kSum
+// brings both ends inside FP32: 2^24 tokens of zeros at the slack, 2^32 at the
+// reference, stay finite, and the other end stays normal.
 #pragma once
 
 #include "cache.h"
@@ -20,6 +24,8 @@
 namespace hwr {
 
 constexpr float kHead = 7.f;    // weights are 2^kHead at the reference
+constexpr float kSum = 12.f;    // bits that the row's sum is held lower by
+constexpr float kSumUnit = 0x1p-12f;  // 2^-kSum
 constexpr float kSlack = 8.f;   // a row's reference rises once it is exceeded by this much
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -248,6 +254,16 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// 2^-kSum / vs, of log2 vs (2^-132 for the largest scale: not flushed).
+__device__ __forceinline__ float inverse_scale(float lvs) { return ex2(-lvs) * kSumUnit; }
+// The square root of 2^{m - to}, the factor from reference m to reference `to` >= m:
+// sums are multiplied by it twice, since the factor alone may be flushed where a
+// sum of tiny value scales still counts.  0 where nothing was seen (m = -inf < to).
+__device__ __forceinline__ float root_factor(float m, float to) { return m == to ? 1.f : ex2((m - to) * 0.5f); }
+// A row's log-sum-exp.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return m == -INFINITY ? -INFINITY : kLn2 * (m - kHead + kSum + log2f(l));
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
   const int n = on ? 16 : 0;  // 0: the 16 bytes become zero, nothing is read

@@ -218,8 +218,8 @@ __device__ __forceinline__ void store_rows(const AttendParams& p, const Tile& x,
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float2 v = ml[w * R + i];
-      const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
-      l += f * v.y;
+      const float h = root_factor(v.x, m), f = h * h;
+      l += v.y * h * h;
       if (v.x != -INFINITY) {  // (a part of a vanishing factor counts, for its NaN)
         const float* a = acc + (w * R + i) * (D + 4) + d;
 #pragma unroll
@@ -231,10 +231,12 @@ __device__ __forceinline__ void store_rows(const AttendParams& p, const Tile& x,
       const int64_t at = (x.q0 + pair / p.G) * static_cast<int64_t>(p.Hq) + h * p.G + pair % p.G;
       const float inv = m == -INFINITY ? 0.f : 1.f / l;
       uint4 v;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] *= kSumUnit;
       v.x = pack_act<F16>(o[0] * inv, o[1] * inv), v.y = pack_act<F16>(o[2] * inv, o[3] * inv);
       v.z = pack_act<F16>(o[4] * inv, o[5] * inv), v.w = pack_act<F16>(o[6] * inv, o[7] * inv);
       *reinterpret_cast<uint4*>(p.out + (at * D + d) * 2) = v;
-      if (p.lse && d == 0) p.lse[at] = m == -INFINITY ? -INFINITY : kLn2 * (m - kHead + log2f(l));
+      if (p.lse && d == 0) p.lse[at] = row_lse(m, l);
     } else {
       float* dst = p.part_o + (part * R + i) * D + d;
       *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
@@ -339,7 +341,7 @@ __device__ void segment(const AttendParams& p, const Tile& x, int h, int u0, int
     const int4 ea = *reinterpret_cast<const int4*>(te + g), eb = *reinterpret_cast<const int4*>(te + g + 8);
     const float ks[2] = {__int_as_float(ea.z), __int_as_float(eb.z)};
     const float lvs[2] = {__int_as_float(ea.w), __int_as_float(eb.w)};
-    const float ivs[2] = {ex2(-lvs[0]), ex2(-lvs[1])};
+    const float ivs[2] = {inverse_scale(lvs[0]), inverse_scale(lvs[1])};
     const int pos[2] = {ea.y, eb.y};
     bool up = false;
 #pragma unroll
@@ -362,9 +364,9 @@ __device__ void segment(const AttendParams& p, const Tile& x, int h, int u0, int
           float top = fmaxf(m[nt][j], fmaxf(sc[nt][j], sc[nt][2 + j]));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-          const float f = top == m[nt][j] ? 1.f : ex2(m[nt][j] - top);
+          const float h = root_factor(m[nt][j], top), f = h * h;
           m[nt][j] = top;
-          l[nt][j] *= f;
+          l[nt][j] *= h, l[nt][j] *= h;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) acc[i][nt][j] *= f, acc[i][nt][2 + j] *= f;
         }
@@ -501,8 +503,8 @@ __device__ __forceinline__ void add_parts(const AttendParams& p, int first, int 
       const float2 w = __ldcg(reinterpret_cast<const float2*>(p.part_o + at * D + d));
       a[0] = w.x, a[1] = w.y;
     }
-    const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
-    l += f * v.y;
+    const float h = root_factor(v.x, m), f = h * h;
+    l += v.y * h * h;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e)
       if (v.x != -INFINITY) o[e] += f * a[e];
@@ -539,8 +541,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float2 v = ml[k];
-        const float f = v.x == -INFINITY ? 0.f : ex2(v.x - m);
-        l += f * v.y;
+        const float h = root_factor(v.x, m), f = h * h;
+        l += v.y * h * h;
 #pragma unroll
         for (int e = 0; e < kN; ++e)
           if (v.x != -INFINITY) o[e] += f * sum[k][d + e];
@@ -551,8 +553,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const float inv = m == -INFINITY ? 0.f : 1.f / l;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (at * D + d) * 2);
 #pragma unroll
-    for (int e = 0; e < kN; e += 2) dst[e / 2] = pack_act<F16>(o[e] * inv, o[e + 1] * inv);
-    if (p.lse && lane == 0) p.lse[at] = m == -INFINITY ? -INFINITY : kLn2 * (m - kHead + log2f(l));
+    for (int e = 0; e < kN; e += 2) dst[e / 2] = pack_act<F16>(o[e] * kSumUnit * inv, o[e + 1] * kSumUnit * inv);
+    if (p.lse && lane == 0) p.lse[at] = row_lse(m, l);
   }
 }
 

@@ -225,7 +225,7 @@ __device__ __forceinline__ void look_up(const AttendParams& p, const Segment& g,
         const int k = e * 32 + en;
         const bool on = at[e].pos != INT32_MAX;
         const float lvs = on ? __log2f(fmaxf(vs[e], kMinBlockScale)) : -INFINITY;
-        const float ivs = on ? ex2(-lvs) : 0.f;
+        const float ivs = on ? inverse_scale(lvs) : 0.f;
         if (U16)
           reinterpret_cast<float4*>(sc)[k] = make_float4(ks[e], lvs, ivs, 0.f);
         else
@@ -593,9 +593,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t tm_s, uint32_t tm_o, const
   tmem_ld_x16(tm_s, a);
   const bool up = top > row.m + kSlack;  // (a row's own affair: its results do not depend on its neighbours)
   if (__any_sync(kFullMask, up)) {
-    const float m = up ? top : row.m, f = up ? ex2(row.m - m) : 1.f;
+    const float m = up ? top : row.m, h = root_factor(row.m, m), f = h * h;
     row.m = m;
-    row.l *= f;
+    row.l *= h, row.l *= h;
     if (!fresh) {
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
@@ -639,12 +639,12 @@ __device__ __forceinline__ void write_rows(const AttendParams& p, const Segment&
   if (whole) {
     const int pair = g.x.first + i, query = pair / p.G;
     at = (g.x.q0 + query) * p.Hq + g.h * p.G + pair - query * p.G;
-    if (p.lse && lane < count) p.lse[at] = none ? -INFINITY : kLn2 * (row.m - kHead + log2f(row.l));
+    if (p.lse && lane < count) p.lse[at] = row_lse(row.m, row.l);
   } else {
     at = static_cast<int>(g.part) * R + i;
     if (lane < count) p.part_ml[at] = make_float2(row.m, row.l);
   }
-  const float mul = !whole ? 1.f : none ? 0.f : 1.f / row.l;
+  const float unit = whole ? kSumUnit : 1.f, mul = !whole ? 1.f : none ? 0.f : 1.f / row.l;
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row of the stage
   const uint32_t mine = stage + lane * (2 * D), sw = lane & 7;
 #pragma unroll 1
@@ -653,7 +653,7 @@ __device__ __forceinline__ void write_rows(const AttendParams& p, const Segment&
     get(c, o);
     const uint32_t bits = nan[c];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = bits >> e & 1 ? NAN : o[e] * mul;
+    for (int e = 0; e < 32; ++e) o[e] = bits >> e & 1 ? NAN : o[e] * unit * mul;
     if (whole) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -797,8 +797,9 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
     // (outputs of a stream that saw nothing may be anything; those of a vanishing
     // factor count, for their NaN)
     const bool on0 = row.m != -INFINITY, on1 = other.x != -INFINITY;
-    const float f0 = on0 ? ex2(row.m - m) : 0.f, f1 = on1 ? ex2(other.x - m) : 0.f;
-    row.l = f0 * row.l + f1 * other.y;  // (NaN where either is, whatever the factors)
+    const float h0 = root_factor(row.m, m), h1 = root_factor(other.x, m), f0 = h0 * h0, f1 = h1 * h1;
+    // (NaN where either is, whatever the factors)
+    row.l = row.l * h0 * h0 + other.y * h1 * h1;
     row.m = m;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) row_nan[e] |= row_nan[128 * 4 + e];

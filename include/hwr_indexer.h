@@ -476,8 +476,11 @@ indexer_status indexer_cache_append(const indexer_cache* cache, const indexer_se
  * Calls with the same shapes and contents give the same bits.
  * Scores, softmax statistics and sums are FP32; the probabilities are
  * rounded to FP16 (relative to the largest seen, with 2^-31 of it as the least),
- * as a factor of the value products only.  The value scales
- * of one sequence may span a factor of 2^120. */
+ * as a factor of the value products only.
+ * Value scales lie from 2^-100 (smaller ones are read as that) to 2^120.  Of a
+ * sequence whose value scales span 2^s, tokens less likely than 2^(s-132) times
+ * the likeliest may be left out of the row's sum; 2^24 tokens and more of zero
+ * values, in blocks of scale 2^-100, do not overflow it. */
 typedef struct {
   int32_t Hq;         /* query heads: a multiple of the cache's heads, at most 128 times as many */
   int32_t act;        /* indexer_act of q and out */

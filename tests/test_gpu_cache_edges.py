@@ -1,6 +1,6 @@
 """Edges of the cache operators on the GPU: scales that are no power of two, NaN
 codes in tiles that only some rows see whole, beside large scores and of vanishing
-weight."""
+weight, runs of zero values."""
 
 import numpy as np
 import pytest
@@ -107,7 +107,8 @@ def _ramp(rng, kv, heads, D, low):
     by_page = np.empty((pages, page), dtype=np.uint8)
     by_page[table[0]] = flat.reshape(pages, page)
     cache.k.copy_(_dev(by_page)[:, :, None, None].expand(pages, page, heads, D))
-    cache.v.copy_(_dev(R.to_code(np.clip(rng.normal(size=(pages, page, heads, D)) * 60, -448, 448))))
+    values = R.to_code(np.clip(rng.normal(size=(64, page, heads, D)) * 60, -448, 448))
+    cache.v.copy_(_dev(np.resize(values, (pages, page, heads, D))))
     cache.k_scale.fill_(2.0 ** -4)
     cache.v_scale.fill_(2.0 ** -6)
     return cache, table
@@ -147,3 +148,63 @@ def test_nan_value_of_vanishing_weight(cuda_ok, kernel, kv, every, part):
     out = I.cache_attend(cache, q, _ints([0, 1]), _ints([kv]), _dev(table), scale=0.2, max_q=1, kernel=kernel)
     nan = out.isnan()
     assert nan[0, 8:, 21].all() and nan.sum() == 8
+
+
+@pytest.mark.parametrize("kernel,B,n,ones", [(STREAM, 300, 14, 0), (TILE, 1200, 14, 0), (STREAM, 300, 19, 64), (TILE, 1200, 16, 64),
+                                             (STREAM, 1, 14, 64), (TILE, 1, 14, 64), (STREAM, 1, 21, 0), (TILE, 1, 21, 0)])
+def test_run_of_zero_values_at_the_slack(cuda_ok, kernel, B, n, ones):
+    """Blocks of zero values have the scale 2^-100.  2^n of their tokens, which score
+    just under what would raise the reference that the first 256 set, then some
+    values that are not zero: sums stay finite.  B sequences over the same
+    pages: with many, one CTA goes over all of the keys."""
+    I = _I()
+    rng = np.random.default_rng(34)
+    kv, D, G = 2 ** n + 256 + 64, 64, 8
+    low = np.where(np.arange(kv) < 256, 0.0, 15.0)         # 15/16 * 64 dimensions * scale below: 7.5 in base 2
+    cache, table = _ramp(rng, kv, 1, D, low)
+    cache.v.zero_()
+    cache.v_scale.fill_(2.0 ** -100)
+    scale = 7.5 * np.log(2) / 60
+    for p in range(kv - ones, kv):
+        cache.v[table[0, p // 64], p % 64] = 0x38 + (p & 1)
+        cache.v_scale[table[0, p // 64], p % 64 // 16] = 1.0
+    q = torch.ones(B, G, D, dtype=torch.bfloat16, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    out, lse = I.cache_attend(cache, q, cu, _ints([kv] * B), _dev(table).expand(B, -1).contiguous(), scale=scale,
+                              with_lse=True, max_q=1, kernel=kernel)
+    # all dimensions are alike: scores 0 and 7.5 ln 2, values 1 and 1.125 in turn
+    total = 256 + (kv - 256) * 2.0 ** 7.5
+    want = 2.0 ** 7.5 * ones * 1.0625 / total
+    # a row's sum is of kv/16 additions one after another or fewer, each within 2^-24;
+    # scores as in the other tests (5.2 at most); weights to FP16, the output to bf16
+    off = kv / 16 * 2.0 ** -24 + 2.0 ** -17
+    assert (np.abs(R.to_np(lse) - np.log(total)) <= off + 2.0 ** -20).all()
+    assert (np.abs(R.to_np(out) - want) <= want * (2.0 ** -8 + 2 * (off + 2.0 ** -12))).all()
+    assert (out == out[:1]).all() and (lse == lse[:1]).all()
+
+
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+@pytest.mark.parametrize("first", [True, False])
+def test_zero_values_count_beside_a_far_larger_scale(cuda_ok, kernel, first):
+    """2^18 tokens of zero values, each 2^-27 as likely as one token whose values'
+    scale is 2^100 times theirs: 1/512 of the row's sum together."""
+    I = _I()
+    rng = np.random.default_rng(36)
+    kv, D, G = 2 ** 18 + 1, 64, 8
+    at = kv - 1 if first else 0
+    low = np.zeros(kv)
+    low[at] = 15.0
+    cache, table = _ramp(rng, kv, 1, D, low)
+    cache.v.zero_()
+    cache.v_scale.fill_(2.0 ** -100)
+    cache.v[table[0, at // 64], at % 64] = 0x38
+    cache.v_scale[table[0, at // 64], at % 64 // 16] = 1.0
+    scale = 27 * np.log(2) / 60
+    q = torch.ones(1, G, D, dtype=torch.bfloat16, device="cuda")
+    out, lse = I.cache_attend(cache, q, _ints([0, 1]), _ints([kv]), _dev(table), scale=scale, with_lse=True, max_q=1,
+                              kernel=kernel)
+    # the score of 18.7 is within 2^-16; the sum's additions, at most kv/16 of them for
+    # 1/512 of it, within a quarter of that
+    rest = np.log1p((kv - 1) * 2.0 ** -27)
+    assert (np.abs(R.to_np(lse) - 27 * np.log(2) - rest) <= rest * 2.0 ** -2).all()
+    assert (np.abs(R.to_np(out) - np.exp(-rest)) <= 2.0 ** -8 + 2.0 ** -11).all()
