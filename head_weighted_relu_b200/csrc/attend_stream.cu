@@ -355,15 +355,17 @@ __device__ void segment(const AttendParams& p, const Tile& x, int h, int u0, int
           sc[nt][2 * t + j] = u;
           up = up || u > m[nt][j] + kSlack;
         }
-    // A row's reference rises to its largest score when that exceeds it by the slack.
+    // A row's reference rises to its largest score when that exceeds it by the slack
+    // (a row's own affair: its results do not depend on its neighbours).
     if (__any_sync(kFullMask, up)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float top = fmaxf(m[nt][j], fmaxf(sc[nt][j], sc[nt][2 + j]));
+          float top = fmaxf(sc[nt][j], sc[nt][2 + j]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+          if (!(top > m[nt][j] + kSlack)) top = m[nt][j];
           const float h = root_factor(m[nt][j], top), f = h * h;
           m[nt][j] = top;
           l[nt][j] *= h, l[nt][j] *= h;

@@ -1,6 +1,6 @@
 """Edges of the cache operators on the GPU: scales that are no power of two, NaN
 codes in tiles that only some rows see whole, beside large scores and of vanishing
-weight, runs of zero values."""
+weight, runs of zero values, rows beside very different ones."""
 
 import numpy as np
 import pytest
@@ -208,3 +208,29 @@ def test_zero_values_count_beside_a_far_larger_scale(cuda_ok, kernel, first):
     rest = np.log1p((kv - 1) * 2.0 ** -27)
     assert (np.abs(R.to_np(lse) - 27 * np.log(2) - rest) <= rest * 2.0 ** -2).all()
     assert (np.abs(R.to_np(out) - np.exp(-rest)) <= 2.0 ** -8 + 2.0 ** -11).all()
+
+
+@pytest.mark.parametrize("G,kernel", [(3, STREAM), (8, STREAM), (3, TILE), (8, TILE)])
+def test_rows_do_not_depend_on_their_neighbours(cuda_ok, G, kernel):
+    """Queries of one sequence share a tile, and their CTAs go over many keys each:
+    another query's values, large or not, change no bit of a row."""
+    I = _I()
+    g = torch.Generator(device="cuda").manual_seed(33)
+    pages, D = 3000, 128
+    cache = I.allocate_cache(pages, 64, 1, D, 16)
+    for x in (cache.k, cache.v):
+        x.copy_((60 * torch.randn(x.shape, generator=g, device="cuda")).clamp(-448, 448).to(torch.float8_e4m3fn)
+                .view(torch.uint8))
+    for x in (cache.k_scale, cache.v_scale):
+        x.fill_(2.0 ** -6)
+    table = torch.randperm(pages, generator=g, device="cuda").int().view(1, pages)
+    for n_q in (2, 5):
+        args = (_ints([0, n_q]), _ints([pages * 64]), table)
+        q = torch.randn(n_q, G, D, generator=g, device="cuda").bfloat16()
+        want, wl = I.cache_attend(cache, q, *args, kernel=kernel, with_lse=True)
+        for i in range(n_q):
+            other = q.clone()
+            other[i] *= 50
+            got, gl = I.cache_attend(cache, other, *args, kernel=kernel, with_lse=True)
+            keep = [j for j in range(n_q) if j != i]
+            assert torch.equal(got[keep], want[keep]) and torch.equal(gl[keep], wl[keep])
