@@ -644,7 +644,7 @@ __device__ __forceinline__ void write_rows(const AttendParams& p, const Segment&
     at = static_cast<int>(g.part) * R + i;
     if (lane < count) p.part_ml[at] = make_float2(row.m, row.l);
   }
-  const float unit = whole ? kSumUnit : 1.f, mul = !whole ? 1.f : none ? 0.f : 1.f / row.l;
+  const float unit = whole ? kSumUnit : 1.f, mul = whole ? 1.f / row.l : 1.f;
   constexpr int kChunks = D / 8;  // 16-byte chunks of a row of the stage
   const uint32_t mine = stage + lane * (2 * D), sw = lane & 7;
 #pragma unroll 1
@@ -653,7 +653,7 @@ __device__ __forceinline__ void write_rows(const AttendParams& p, const Segment&
     get(c, o);
     const uint32_t bits = nan[c];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = bits >> e & 1 ? NAN : o[e] * unit * mul;
+    for (int e = 0; e < 32; ++e) o[e] = bits >> e & 1 ? NAN : none ? 0.f : o[e] * unit * mul;
     if (whole) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -686,6 +686,17 @@ __device__ __forceinline__ void write_rows(const AttendParams& p, const Segment&
     }
     __syncwarp();
   }
+}
+
+// Whether row i of the segment's tile sees a token in it.  For rows of NaN alone,
+// whose queries may be anything: padding rows too.
+__device__ __forceinline__ bool sees_any(const AttendParams& p, const Segment& g, int i) {
+  const int end = min(g.x.n_keys, (g.u0 + g.n) * kKeys), limit = row_limit(p, g.x, g.x.first + i);
+  const Translate tr(p, g.x, g.h, end);
+#pragma unroll 1
+  for (int e = g.u0 * kKeys; e < end; ++e)
+    if (tr.place(tr.page(tr.index(e))).pos < limit) return true;
+  return false;
 }
 
 template <int D, int NM, bool U16>
@@ -761,7 +772,12 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
   wait(bars, &bars->ofull, segs & 1);
   tc_fence_after();
   if (*reinterpret_cast<volatile int*>(&bars->abort)) row.l = NAN;
-  if (isnan(row.l)) row.m = 0.f;  // a row of NaN scores counts in a join
+  if (isnan(row.l)) {
+    if (row.m == -INFINITY && !sees_any(p, g, i))
+      row.l = 0.f;  // (its query times the zeros of tokens that are none)
+    else
+      row.m = 0.f;  // a row of NaN scores counts in a join
+  }
   const uint32_t stage = smem_u32(smem) + L::kQ + (threadIdx.x >> 5) * (64 * D);  // (all products are done)
   if (NM == 2) {
     if (busy)

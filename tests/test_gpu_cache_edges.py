@@ -1,6 +1,7 @@
 """Edges of the cache operators on the GPU: scales that are no power of two, NaN
 codes in tiles that only some rows see whole, beside large scores and of vanishing
-weight, runs of zero values, rows beside very different ones."""
+weight, runs of zero values, rows beside very different ones,
+rows that see nothing."""
 
 import numpy as np
 import pytest
@@ -234,3 +235,34 @@ def test_rows_do_not_depend_on_their_neighbours(cuda_ok, G, kernel):
             got, gl = I.cache_attend(cache, other, *args, kernel=kernel, with_lse=True)
             keep = [j for j in range(n_q) if j != i]
             assert torch.equal(got[keep], want[keep]) and torch.equal(gl[keep], wl[keep])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+@pytest.mark.parametrize("G,block", [(8, 16), (64, 8)])
+def test_rows_that_see_nothing_whatever_their_query(cuda_ok, kernel, G, block, bad):
+    """Padding rows whose queries hold anything: nothing selected, nothing but unseen
+    or missing tokens selected, no page, a length of zero."""
+    I = _I()
+    rng = np.random.default_rng(35)
+    cache, table = _filled(rng, [200, 200, 64], 1, 128, 32, block)
+    table[1, :] = -1
+    q = _dev(rng.normal(size=(5, G, 128)), torch.bfloat16)
+    clean = q.clone()
+    q[[0, 1, 3, 4]] = bad
+    cu, kv = _ints([0, 3, 4, 5]), _ints([200, 200, 0])
+    idx = np.full((5, 300), -1, dtype=np.int32)
+    idx[1, :3] = [199, 200, -7]                            # row 1 sees up to 198
+    idx[2, :150] = np.arange(150)
+    idx[3, :100] = np.arange(100)
+    idx[4, :2] = [0, 1]
+    ln = _ints([0, 3, 150, 100, 2])
+    tb = _dev(table)
+    for kw in (dict(selected=(_dev(idx), ln)), dict()):
+        out, lse = I.cache_attend(cache, q, cu, kv, tb, with_lse=True, kernel=kernel, **kw)
+        want, wl = I.cache_attend(cache, clean, cu, kv, tb, with_lse=True, kernel=kernel, **kw)
+        empty = [0, 1, 3, 4] if kw else [3, 4]
+        assert (out[empty] == 0).all() and lse[empty].isneginf().all()
+        assert torch.equal(out[2], want[2]) and torch.equal(lse[2], wl[2]) and out[2].isfinite().all()
+        if not kw:
+            assert out[:2].isnan().all()
