@@ -119,6 +119,7 @@ indexer_status plan_attend(const indexer_cache* c, const indexer_sequences* s, c
   p.causal = a->causal;
   p.sel_width = a->sel_width;
   p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
+  if (!isfinite(p.scale_log2)) return INDEXER_EINVAL;
   pl->f16 = a->act == INDEXER_ACT_FP16;
   pl->D = c->D;
   int sms = 0;

@@ -488,7 +488,7 @@ typedef struct {
   int32_t sel_width;  /* 0: no selection */
   int32_t max_q;      /* rows of the longest sequence, or 0 if unknown: it
                          chooses the kernel, and so may change roundings */
-  float scale;        /* finite */
+  float scale;        /* finite, and so is scale * log2(e) */
   int32_t kernel;     /* indexer_attend_kernel: a given one does not depend on the
                          batch, and a row's result in it only on how its keys are
                          divided */
