@@ -1,7 +1,8 @@
 """Edges of the cache operators on the GPU: scales that are no power of two, NaN
 codes in tiles that only some rows see whole, beside large scores and of vanishing
 weight, runs of zero values, rows beside very different ones,
-rows that see nothing."""
+rows that see nothing; large ragged batches, pages interleaved by token, results in
+the place of their inputs, large appends in a graph."""
 
 import numpy as np
 import pytest
@@ -266,3 +267,93 @@ def test_rows_that_see_nothing_whatever_their_query(cuda_ok, kernel, G, block, b
         assert torch.equal(out[2], want[2]) and torch.equal(lse[2], wl[2]) and out[2].isfinite().all()
         if not kw:
             assert out[:2].isnan().all()
+
+
+# ----------------------------------------- calls that other tests do not make --
+
+@pytest.mark.parametrize("kernel", [STREAM, TILE])
+def test_ragged_decode_batch_of_many_sequences(cuda_ok, kernel):
+    """More sequences than CTAs of the streaming kernel share: one long context among
+    short ones, some of them empty."""
+    I = _I()
+    rng = np.random.default_rng(41)
+    B, D = 300, 128
+    kv = rng.integers(0, 60, size=B).tolist()
+    kv[17] = 3000
+    cache, table = _filled(rng, kv, 2, D, 64, 16)
+    cu = np.arange(B + 1, dtype=np.int32)
+    q = _dev(rng.normal(size=(B, 16, D)), torch.bfloat16)
+    out, lse = I.cache_attend(cache, q, _dev(cu), _ints(kv), _dev(table), with_lse=True, max_q=1, kernel=kernel)
+    _check_attend(cache, q, cu, kv, table, D ** -0.5, True, None, out, lse, "bf16")
+
+
+def test_pages_interleaved_by_token(cuda_ok):
+    """Memory [tokens of a page, pages, heads, D], and [heads, pages, tokens, D]: the
+    same cache and the same attention as page by page."""
+    I = _I()
+    g = torch.Generator(device="cuda").manual_seed(42)
+    pages, page, heads, D, n = 7, 32, 3, 64, 200
+    k, v = (torch.randn(n, heads, D, generator=g, device="cuda").half() for _ in range(2))
+    q = torch.randn(n, 2 * heads, D, generator=g, device="cuda").half()
+    table = torch.randperm(pages, generator=g, device="cuda").int().view(1, pages)
+    rt = I.rope_table(n, 64)
+    results = []
+    for order in ((0, 1, 2), (1, 0, 2), (2, 0, 1)):
+        sizes = [(pages, page, heads)[i] for i in order]
+        codes = [torch.zeros(*sizes, D, dtype=torch.uint8, device="cuda").permute(*[order.index(i) for i in range(3)], 3)
+                 for _ in range(2)]
+        scales = [torch.zeros(pages, page // 16, heads, device="cuda") for _ in range(2)]
+        cache = I.KVCache(*codes, *scales)
+        for a, b in ((0, 77), (77, n)):
+            I.cache_append(cache, k[a:b], v[a:b], _ints([0, b - a]), _ints([b]), table, table=rt)
+        results.append([x.contiguous() for x in cache] + [I.cache_attend(cache, q, _ints([0, n]), _ints([n]), table, kernel=x)
+                                                          for x in (STREAM, TILE)])
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_results_in_the_place_of_their_inputs(cuda_ok, inter):
+    """q rotated, and attended with, in its own memory; q large enough for a kernel
+    of its own in one case."""
+    I = _I()
+    g = torch.Generator(device="cuda").manual_seed(43)
+    for n, Hq, rot in ((50, 16, 48), (1100, 128, 128)):
+        cache = I.allocate_cache(-(-n // 64), 64, 4, 128, 16)
+        table = torch.arange(cache.k.shape[0], dtype=torch.int32, device="cuda").view(1, -1)
+        k = torch.randn(n, 4, 128, generator=g, device="cuda").bfloat16()
+        q = torch.randn(n, Hq, 128, generator=g, device="cuda").bfloat16()
+        args = (_ints([0, n]), _ints([n]), table)
+        want = I.cache_append(cache, k, k, *args, table=I.rope_table(n, rot), interleaved=inter, q=q)
+        same = q.clone()
+        assert I.cache_append(cache, k, k, *args, table=I.rope_table(n, rot), interleaved=inter, q=same, q_out=same) is same
+        assert torch.equal(same, want)
+        for kernel in (STREAM, TILE):
+            x = want.clone()
+            out = I.cache_attend(cache, want, *args, kernel=kernel)
+            assert torch.equal(I.cache_attend(cache, x, *args, kernel=kernel, out=x), out)
+
+
+def test_large_append_in_a_graph(cuda_ok):
+    """q in a kernel of its own, captured and replayed with other rows and lengths,
+    and what follows it in the graph."""
+    I = _I()
+    g = torch.Generator(device="cuda").manual_seed(44)
+    n, Hq, heads, D = 1100, 128, 2, 128
+    one, two = (I.allocate_cache(40, 64, heads, D, 64) for _ in range(2))
+    table = torch.randperm(40, generator=g, device="cuda").int().view(1, 40)
+    rt = I.rope_table(40 * 64, 128)
+    q, k, v = (torch.empty(n, h, D, dtype=torch.bfloat16, device="cuda") for h in (Hq, heads, heads))
+    cu, kv = _ints([0, n]), _ints([n])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q_rot = I.cache_append(one, k, v, cu, kv, table, table=rt, q=q)
+        out = I.cache_attend(one, q_rot, cu, kv, table)
+    for length in (n, 2 * n):
+        for x in (q, k, v):
+            x.normal_(generator=g)
+        kv.fill_(length)
+        graph.replay()
+        want = I.cache_append(two, k, v, cu, kv, table, table=rt, q=q)
+        assert torch.equal(q_rot, want)
+        assert torch.equal(out, I.cache_attend(two, want, cu, kv, table))
