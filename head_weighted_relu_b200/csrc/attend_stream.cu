@@ -24,8 +24,9 @@
 // took the heads of a token to be read side by side (CTAs c, c + 1, .. on the same
 // keys): a head alone is 128 bytes of every 1,024, 258 us.  One entry for 16
 // tokens that share their scales, instead of one each, changed nothing.  1,024
-// rows over 2,048 selected tokens each of 16,384 (the cache in L2): 578 us, 7.4
-// TB/s out of L2.
+// rows over 2,048 selected tokens each of 16,384 (the cache in L2): 587 us, 7.3
+// TB/s out of L2, a third of what L2 gives: issue slots 62% busy and the integer pipe
+// 54%, with four warps an SM quarter.
 #include "attend.cuh"
 
 namespace hwr {

@@ -25,9 +25,10 @@
 // softmax (2,100 alone, 2,800 beside the other's, 3,000 to 3,400 beside the
 // fill) and its products (1,100 and the hand-overs) follow one another, and two
 // streams do not cover all of each other.  2,048 rows over 16,384 tokens, 64
-// heads on 8: 1.18 ms, 875 TFLOP/s (1.24 ms call after call, at the power limit:
-// 1,850 MHz).  One stream's rows, NM = 1: one query of 64
-// heads over 1,048,576 tokens 109 us, 2.5 TB/s.
+// heads on 8: 1.19 ms, 866 TFLOP/s (1.27 ms call after call, at the power limit;
+// 41% of the tensor pipe's cycles, 41% of the exponential pipe's).  One stream's
+// rows, NM = 1: one query of 64 heads over 1,048,576 tokens 112 us, 2.4 TB/s (33%
+// of the tensor pipe's cycles).
 // Tried and worse: scores in halves of 64 keys, so that products run during the
 // softmax (the halves' products re-read the queries: 1.34 ms); one pass that
 // keeps the weights in registers, or takes no maximum until a sum overflows (1.35

@@ -11,9 +11,9 @@
 // Measured: FP8 rows of 16,384 tokens x 64 heads x 128, 64 dimensions rotated:
 // 99 us for 407 MB, 4.1 TB/s; the integer pipe is busy 67% of the time (16-bit
 // values unpacked, row maxima, codes packed: half-rate instructions), the issue
-// slots 70%.  The append of 8,192 tokens (64 heads of q, 8 of k and v): q 42 us
-// for 268 MB, 6.4 TB/s, as a copy; keys and values 25 us for 50 MB, bound by
-// latency (16 warps an SM at 128 registers).
+// slots 70%.  The append of 8,192 tokens (64 heads of q, 8 of k and v): 68 us,
+// of which q 42 for 268 MB, 6.4 TB/s, as a copy; keys and values, 50 MB, the rest,
+// bound by latency (16 warps an SM at 128 registers).
 #include "cache.h"
 
 namespace hwr {

@@ -660,6 +660,7 @@ def cache_attend(cache: KVCache, q, cu_q, kv_len, page_table, scale=None, causal
     the positions named.  A row that sees nothing gives 0 and -inf.  scale
     defaults to D ** -0.5.  max_q: rows of the longest sequence, if known (it
     chooses the kernel: results may differ by roundings; or name it by `kernel`).
+    Left at 0, all S rows count as one sequence's: give it for a batch.
     workspace: a uint8 tensor kept by the caller (its size from
     `cache_attend_workspace_bytes`); by default it is allocated for the call.
     """

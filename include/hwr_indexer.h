@@ -486,8 +486,10 @@ typedef struct {
   int32_t act;        /* indexer_act of q and out */
   int32_t causal;     /* 0 or 1 */
   int32_t sel_width;  /* 0: no selection */
-  int32_t max_q;      /* rows of the longest sequence, or 0 if unknown: it
-                         chooses the kernel, and so may change roundings */
+  int32_t max_q;      /* rows of the longest sequence, or 0 if unknown (S is
+                         taken then, which for a batch may be the slower
+                         kernel): it chooses the kernel, and so may change
+                         roundings */
   float scale;        /* finite, and so is scale * log2(e) */
   int32_t kernel;     /* indexer_attend_kernel: a given one does not depend on the
                          batch, and a row's result in it only on how its keys are
