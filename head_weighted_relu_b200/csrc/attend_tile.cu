@@ -779,6 +779,7 @@ __device__ __forceinline__ void softmax(const AttendParams& p, const Segment& se
     else
       row.m = 0.f;  // a row of NaN scores counts in a join
   }
+  __syncwarp();  // (the rows' accesses to TMEM are the warp's together)
   const uint32_t stage = smem_u32(smem) + L::kQ + (threadIdx.x >> 5) * (64 * D);  // (all products are done)
   if (NM == 2) {
     if (busy)
